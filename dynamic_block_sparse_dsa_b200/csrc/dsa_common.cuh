@@ -107,4 +107,36 @@ __device__ __forceinline__ int atomic_add_acq_rel_gpu(int32_t *p, int v) {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" :::); }
 
+// Loads of what a kernel before this one wrote (coarse keys, scores,
+// selections, scales), for use after pdl_wait().  They are volatile because the
+// compiler may move a read-only-path load (__ldg) or a plain __ldcg up across
+// the wait, which is an opaque instruction to it: the load then reads memory
+// that the earlier kernel is still writing.
+__device__ __forceinline__ int ld_ordered(const int *p) {
+    int v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int4 ld_ordered(const int4 *p) {
+    int4 v;
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ long long ld_ordered(const long long *p) {
+    long long v;
+    asm volatile("ld.global.b64 %0, [%1];" : "=l"(v) : "l"(p));
+    return v;
+}
+// the same through L2 alone (data read once, or written while this kernel runs)
+__device__ __forceinline__ int ld_ordered_cg(const int *p) {
+    int v;
+    asm volatile("ld.global.cg.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float ld_ordered_cg(const float *p) {
+    float v;
+    asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
 }  // namespace dsa

@@ -14,7 +14,7 @@ __device__ __forceinline__ void load_coarse_key(const int8_t *kc_pool, int page,
     const int4 *src = reinterpret_cast<const int4 *>(kc_pool + (size_t)page * kIdxDim);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int4 v = __ldg(src + i);
+        const int4 v = ld_ordered(src + i);
         kc[4 * i + 0] = v.x; kc[4 * i + 1] = v.y; kc[4 * i + 2] = v.z; kc[4 * i + 3] = v.w;
     }
 }
@@ -55,10 +55,10 @@ __device__ __forceinline__ void tile16_load(const int8_t *kc_pool, int page_g, i
     const int *row_g8 = reinterpret_cast<const int *>(kc_pool + (size_t)max(page_g8, 0) * kIdxDim);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-        f.a[ks][0] = page_g >= 0 ? __ldg(row_g + 8 * ks + c) : 0;
-        f.a[ks][1] = page_g8 >= 0 ? __ldg(row_g8 + 8 * ks + c) : 0;
-        f.a[ks][2] = page_g >= 0 ? __ldg(row_g + 8 * ks + 4 + c) : 0;
-        f.a[ks][3] = page_g8 >= 0 ? __ldg(row_g8 + 8 * ks + 4 + c) : 0;
+        f.a[ks][0] = page_g >= 0 ? ld_ordered(row_g + 8 * ks + c) : 0;
+        f.a[ks][1] = page_g8 >= 0 ? ld_ordered(row_g8 + 8 * ks + c) : 0;
+        f.a[ks][2] = page_g >= 0 ? ld_ordered(row_g + 8 * ks + 4 + c) : 0;
+        f.a[ks][3] = page_g8 >= 0 ? ld_ordered(row_g8 + 8 * ks + 4 + c) : 0;
     }
 }
 

@@ -280,8 +280,8 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const int len = __ldg(a.seq_lens + s);
                 pdl_wait();   // returns at once after the first time
                 // the selection may have been written during this launch: read it through L2
-                int n_sel = sel_ready ? __ldcg(a.cnt + t) : 0;
-                const int b = sel_ready ? __ldcg(a.sel + (size_t)t * a.k_max + j) : -1;
+                int n_sel = sel_ready ? ld_ordered_cg(a.cnt + t) : 0;
+                const int b = sel_ready ? ld_ordered_cg(a.sel + (size_t)t * a.k_max + j) : -1;
                 const int n_vis_blocks = (p >> a.block_shift) + 1;
                 n_vis = (p >> 6) + 1;
                 if (p < 0 || p >= len || n_vis_blocks > a.max_blocks || n_sel < 0 || n_sel > a.k_max) n_sel = 0;

@@ -72,8 +72,8 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(TopkArgs a) {
     // any two differ, so the digits start there
     uint32_t diff = 0;
     {
-        const uint32_t u0 = order_key(__ldg(row));
-        for (int i = tid; i < n; i += kTopkThreads) diff |= order_key(__ldg(row + i)) ^ u0;
+        const uint32_t u0 = order_key(ld_ordered(row));
+        for (int i = tid; i < n; i += kTopkThreads) diff |= order_key(ld_ordered(row + i)) ^ u0;
         diff = __reduce_or_sync(0xffffffffu, diff);
         if (lane == 0) s_warp[0][warp] = diff;
         __syncthreads();
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(TopkArgs a) {
         s_hist[tid] = 0u;
         __syncthreads();   // (also: the previous digit's state has been read by all)
         for (int i = tid; i < n; i += kTopkThreads) {
-            const uint32_t u = order_key(__ldg(row + i));
+            const uint32_t u = order_key(ld_ordered(row + i));
             if ((u & mask) == prefix) atomicAdd(&s_hist[(u >> sh) & dmask], 1u);
         }
         __syncthreads();
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(TopkArgs a) {
     uint32_t n_above = 0, n_tied = 0;
     for (int i0 = i_begin; i0 < i_end; i0 += 32) {
         const int i = i0 + lane;
-        const uint32_t u = i < i_end ? order_key(__ldg(row + i)) & mask : 0u;
+        const uint32_t u = i < i_end ? order_key(ld_ordered(row + i)) & mask : 0u;
         n_above += __popc(__ballot_sync(0xffffffffu, i < i_end && u > prefix));
         n_tied += __popc(__ballot_sync(0xffffffffu, i < i_end && u == prefix));
     }
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(TopkArgs a) {
     const uint32_t lt = (1u << lane) - 1u;
     for (int i0 = i_begin; i0 < i_end; i0 += 32) {
         const int i = i0 + lane;
-        const uint32_t u = i < i_end ? order_key(__ldg(row + i)) & mask : 0u;
+        const uint32_t u = i < i_end ? order_key(ld_ordered(row + i)) & mask : 0u;
         const bool tied = i < i_end && u == prefix;
         const uint32_t mt = __ballot_sync(0xffffffffu, tied);
         const bool take = (i < i_end && u > prefix) || (tied && (whole || tied_before + __popc(mt & lt) < need));

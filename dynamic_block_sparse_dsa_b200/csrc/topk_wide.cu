@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kWtThreads) topk_wide_kernel(TopkArgs a, const
     bool first = true;
     for (int g0 = warp * 64; g0 < n; g0 += kWtWarps * 64) {
         const int i0 = g0 + lane, i1 = g0 + 32 + lane;
-        WKey v[2] = {i0 < n ? wk_make(__ldg(reinterpret_cast<const long long *>(row) + i0), (uint32_t)i0) : kNone,
-                     i1 < n ? wk_make(__ldg(reinterpret_cast<const long long *>(row) + i1), (uint32_t)i1) : kNone};
+        WKey v[2] = {i0 < n ? wk_make(ld_ordered(reinterpret_cast<const long long *>(row) + i0), (uint32_t)i0) : kNone,
+                     i1 < n ? wk_make(ld_ordered(reinterpret_cast<const long long *>(row) + i1), (uint32_t)i1) : kNone};
         if (!first) {
             // keys not above the current kk-th largest cannot reach the first kk
             const WKey thr = wk_from(kk <= 32 ? acc[0] : acc[1], (kk - 1) & 31);
