@@ -10,6 +10,14 @@ the current CUDA stream); all of the method runs in the library's kernels:
     sparse_attn_decode   exact attention over the selected blocks (split-KV)
     sparse_attn_prefill  same, each (query, KV head) pair inside one CTA
 
+rotary positions and the 8-bit cache (PagedKVCacheFP8: E4M3 codes with a scale
+per 64-token tile and KV head):
+
+    kv_append_rope           kv_append with K (and the step's queries) rotated
+    kv_append_fp8            the same into the 8-bit cache, quantised on the way
+    sparse_attn_decode_fp8   the two attention calls over the 8-bit cache
+    sparse_attn_prefill_fp8
+
 and the fused forms: select_blocks (score + Top-K, no score matrix),
 select_blocks_append (the same with the append in one launch, decode),
 decode_fused (a whole decode step in one launch), sparse_attn_decode_noalloc
@@ -38,12 +46,14 @@ __all__ = [
     "kv_append", "index_score", "topk_blocks", "select_blocks", "select_blocks_append", "sparse_attn_decode",
     "sparse_attn_prefill", "decode_fused", "decode_workspace_size", "select_workspace_size",
     "decode_fused_workspace_size", "sparse_attn_decode_noalloc", "step", "PreparedStep", "Stager", "index_score_i64",
-    "index_score_fp8", "topk_blocks_i64",
+    "index_score_fp8", "topk_blocks_i64", "PagedKVCacheFP8", "Rotary", "kv_append_rope", "kv_append_fp8",
+    "sparse_attn_decode_fp8", "sparse_attn_prefill_fp8",
 ]
 
 BLOCK_SIZE = 64
 HEAD_DIM = 128
 IDX_DIM = 64
+TILE = 64   # tokens that share one scale of the 8-bit cache
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -88,6 +98,8 @@ class PagedKVCache:
         return _lib.KvCacheC(_addr(self.k_pool), _addr(self.v_pool), _addr(self.kc_pool), n, bs, hkv, d,
                              self.kc_pool.shape[1])
 
+    index_ctype = ctype
+
     @property
     def num_kv_heads(self) -> int:
         return self.k_pool.shape[2]
@@ -95,6 +107,77 @@ class PagedKVCache:
     @property
     def block_size(self) -> int:
         return self.k_pool.shape[1]
+
+
+@dataclass
+class PagedKVCacheFP8:
+    """Block-paged 8-bit pools: k/v E4M3 codes [num_pages][block_size][num_kv_heads][128]
+    (uint8 or torch.float8_e4m3fn), kc int8 [num_pages][64], k/v_scale fp32
+    [num_pages][block_size / 64][num_kv_heads]; a stored value is code * scale.
+    kv_append_fp8 sets a tile's scale with its first token, so the scales need
+    no initial values.  The indexer and selection calls take this cache as it is."""
+    k_pool: torch.Tensor
+    v_pool: torch.Tensor
+    kc_pool: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    def ctype(self) -> _lib.KvCacheFp8C:
+        kp, vp = self.k_pool, self.v_pool
+        if kp.dtype not in _CODES or vp.dtype not in _CODES:
+            raise ValueError(f"k_pool and v_pool must hold E4M3 codes, got {kp.dtype} and {vp.dtype}")
+        n, bs, hkv, d = kp.shape
+        if vp.shape != kp.shape:
+            raise ValueError("k_pool and v_pool differ in shape")
+        if self.kc_pool.element_size() != 1 or self.kc_pool.shape[0] != n:
+            raise ValueError("kc_pool must hold one byte per element and one row per page")
+        _expect(self.k_scale, torch.float32, "k_scale")
+        _expect(self.v_scale, torch.float32, "v_scale")
+        tiles = (n, bs // TILE, hkv)
+        if self.k_scale.shape != tiles or self.v_scale.shape != tiles:
+            raise ValueError(f"k_scale and v_scale must be {list(tiles)}")
+        return _lib.KvCacheFp8C(_addr(kp), _addr(vp), _addr(self.kc_pool), _addr(self.k_scale), _addr(self.v_scale),
+                                n, bs, hkv, d, self.kc_pool.shape[1])
+
+    def index_ctype(self) -> _lib.KvCacheC:
+        """What the indexer and selection calls read: the coarse keys and the sizes."""
+        c = self.ctype()
+        return _lib.KvCacheC(c.k_pool, c.v_pool, c.kc_pool, c.num_pages, c.block_size, c.num_kv_heads, c.head_dim,
+                             c.idx_dim)
+
+    @property
+    def num_kv_heads(self) -> int:
+        return self.k_pool.shape[2]
+
+    @property
+    def block_size(self) -> int:
+        return self.k_pool.shape[1]
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+@dataclass
+class Rotary:
+    """Rotary positions: inv_freq fp32 [rotary_dim / 2] radians per position.
+    Pairs are dims (i, i + rotary_dim / 2), or (2i, 2i + 1) with ``interleaved``;
+    with ``num_axes`` > 1, pair i turns by the position on axis pair_axis[i]
+    (int32 [rotary_dim / 2]).  ``scale`` multiplies the rotated dims."""
+    inv_freq: torch.Tensor
+    interleaved: bool = False
+    num_axes: int = 1
+    pair_axis: Optional[torch.Tensor] = None
+    scale: float = 1.0
+
+    def ctype(self) -> _lib.RopeC:
+        _expect(self.inv_freq, torch.float32, "inv_freq")
+        half = self.inv_freq.numel()
+        if self.num_axes > 1:
+            if self.pair_axis is None or self.pair_axis.numel() != half:
+                raise ValueError("num_axes > 1 needs pair_axis, one entry per pair")
+            _expect(self.pair_axis, torch.int32, "pair_axis")
+        return _lib.RopeC(_addr(self.inv_freq), _addr(self.pair_axis) if self.num_axes > 1 else None, 2 * half,
+                          1 if self.interleaved else 0, self.num_axes, self.scale)
 
 
 @dataclass
@@ -136,6 +219,118 @@ def kv_append(cache: PagedKVCache, seqs: SeqBatch, cu_new: torch.Tensor, k_new: 
         _ptr(kc_new), _ptr(dev_err), _stream(stream)))
 
 
+def _rows(t: torch.Tensor, heads: Optional[int], name: str):
+    """(address, elements from one token to the next) of bf16 [tokens][heads][128] rows;
+    only the tokens may be apart (slices of a packed projection)."""
+    _expect(t, torch.bfloat16, name)
+    if t.dim() != 3 or t.shape[2] != HEAD_DIM or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens][{'heads' if heads is None else heads}][{HEAD_DIM}], got "
+                         f"{list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("dynamic_block_sparse_dsa_b200 works on CUDA tensors only (no CPU path)")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != HEAD_DIM):
+        raise ValueError(f"the heads of each token of {name} must be contiguous")
+    # a single token has no next one; torch may give it any stride
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * HEAD_DIM
+
+
+def _positions(pos: Optional[torch.Tensor], axes: int, n: int, name: str):
+    if pos is None:
+        return None
+    _expect(pos, torch.int32, name)
+    if pos.numel() != axes * n or pos.shape[-1] != n:
+        raise ValueError(f"{name} must be [{axes}][{n}], got {list(pos.shape)}")
+    return _addr(pos)
+
+
+def _same_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    """Every tensor on one device, which is the current one: the library launches there."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("dynamic_block_sparse_dsa_b200 works on CUDA tensors only (no CPU path)")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"the tensors of one call are on cuda:{dev} and on device {t.get_device()}")
+
+
+def _append_rope(fn: str, c, cache, seqs: SeqBatch, cu_new, k_new, v_new, kc_new, rope, pos_new, queries, q, pos_q, q_out,
+                 dev_err, stream):
+    hkv, axes = cache.num_kv_heads, 1 if rope is None else rope.num_axes
+    total = 0 if k_new is None else k_new.shape[0]
+    fresh = _lib.NewTokensC()
+    if total:
+        k, ks = _rows(k_new, hkv, "k_new")
+        v, vs = _rows(v_new, hkv, "v_new")
+        _expect(cu_new, torch.int32, "cu_new")
+        if v_new.shape[0] != total or cu_new.numel() != seqs.seq_lens.numel() + 1:
+            raise ValueError("v_new must have k_new's tokens, cu_new one entry more than there are sequences")
+        if kc_new is not None and (kc_new.element_size() != 1 or tuple(kc_new.shape) != (total, cache.kc_pool.shape[1])):
+            raise ValueError(f"kc_new must hold one byte per element, [{total}][{cache.kc_pool.shape[1]}]")
+        fresh = _lib.NewTokensC(_addr(cu_new), total, k, v, ks, vs, None if kc_new is None else _addr(kc_new),
+                                _positions(pos_new, axes, total, "pos_new"))
+    rows = qc = None
+    if q is not None:
+        if rope is None or queries is None:
+            raise ValueError("rotating queries needs rope and queries")
+        qp, qs = _rows(q, None, "q")
+        if q.shape[0] != queries.total_q:
+            raise ValueError(f"q has {q.shape[0]} rows for {queries.total_q} queries")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _expect(q_out, torch.bfloat16, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        rows = _lib.QueryRowsC(qp, qs, q.shape[1], _positions(pos_q, axes, q.shape[0], "pos_q"), _addr(q_out))
+        qc = queries.ctype()
+    _same_device(cache.k_pool, cache.v_pool, cache.kc_pool, seqs.block_table, seqs.seq_lens,
+                 *((cu_new, k_new, v_new, kc_new, pos_new) if total else ()),
+                 *((q, q_out, pos_q, queries.q_pos) if q is not None else ()),
+                 *(() if rope is None else (rope.inv_freq, rope.pair_axis)), dev_err)
+    s, r = seqs.ctype(), None if rope is None else rope.ctype()
+    _lib.check(fn, getattr(load(), fn)(
+        ctypes.byref(c), ctypes.byref(s), ctypes.byref(fresh), None if r is None else ctypes.byref(r),
+        None if qc is None else ctypes.byref(qc), None if rows is None else ctypes.byref(rows), _ptr(dev_err),
+        _stream(stream)))
+    return q_out
+
+
+def kv_append_rope(cache: PagedKVCache, seqs: SeqBatch, cu_new: Optional[torch.Tensor], k_new: Optional[torch.Tensor],
+                   v_new: Optional[torch.Tensor], kc_new: Optional[torch.Tensor], rope: Rotary,
+                   pos_new: Optional[torch.Tensor] = None, queries: Optional[QueryBatch] = None,
+                   q: Optional[torch.Tensor] = None, pos_q: Optional[torch.Tensor] = None,
+                   q_out: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None, stream=None):
+    """kv_append with the keys rotated on the way, and the step's queries in
+    the same launch: returns the rotated queries (``q_out``, allocated here if
+    None; None without ``q``).  ``k_new``/``v_new``/``q`` may be slices of a
+    packed projection (only the tokens apart); ``q_out`` may be a contiguous
+    ``q`` itself.  ``pos_new``/``pos_q`` are int32 [num_axes][tokens] positions,
+    by default each token's place in its sequence.  ``k_new`` None: nothing
+    is appended, only the queries are rotated."""
+    if not isinstance(cache, PagedKVCache):
+        raise TypeError("kv_append_rope appends to a PagedKVCache (kv_append_fp8 to a PagedKVCacheFP8)")
+    return _append_rope("dsa_kv_append_rope", cache.ctype(), cache, seqs, cu_new, k_new, v_new, kc_new, rope, pos_new,
+                        queries, q, pos_q, q_out, dev_err, stream)
+
+
+def kv_append_fp8(cache: PagedKVCacheFP8, seqs: SeqBatch, cu_new: Optional[torch.Tensor],
+                  k_new: Optional[torch.Tensor], v_new: Optional[torch.Tensor], kc_new: Optional[torch.Tensor] = None,
+                  rope: Optional[Rotary] = None, pos_new: Optional[torch.Tensor] = None,
+                  queries: Optional[QueryBatch] = None, q: Optional[torch.Tensor] = None,
+                  pos_q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                  dev_err: Optional[torch.Tensor] = None, stream=None):
+    """kv_append_rope into the 8-bit cache, quantised on the way (``rope`` None:
+    the keys are stored as they come).  Each (64-token tile, KV head) has one
+    power-of-two scale for K and one for V, which grows when a new token needs
+    it; the tile's earlier codes are then rounded anew."""
+    if not isinstance(cache, PagedKVCacheFP8):
+        raise TypeError("kv_append_fp8 appends to a PagedKVCacheFP8")
+    _same_device(cache.k_pool, cache.k_scale, cache.v_scale)
+    return _append_rope("dsa_kv_append_fp8", cache.ctype(), cache, seqs, cu_new, k_new, v_new, kc_new, rope, pos_new,
+                        queries, q, pos_q, q_out, dev_err, stream)
+
+
 def index_score(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, q_idx: torch.Tensor,
                 w: torch.Tensor, w_abs_max: int = 16, scores: Optional[torch.Tensor] = None,
                 dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -146,7 +341,7 @@ def index_score(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, q_idx:
     if scores is None:
         scores = torch.empty((queries.total_q, seqs.block_table.shape[1]), dtype=torch.int32,
                              device=q_idx.device)
-    c, s, q = cache.ctype(), seqs.ctype(), queries.ctype()
+    c, s, q = cache.index_ctype(), seqs.ctype(), queries.ctype()
     _lib.check("dsa_index_score", lib.dsa_index_score(
         ctypes.byref(c), ctypes.byref(s), ctypes.byref(q), _ptr(q_idx), _ptr(w), q_idx.shape[1],
         int(w_abs_max), _ptr(scores), _ptr(dev_err), _stream(stream)))
@@ -179,7 +374,7 @@ def index_score_i64(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, q_
     _expect(w, torch.int32, "w")
     if scores is None:
         scores = torch.empty((queries.total_q, seqs.block_table.shape[1]), dtype=torch.int64, device=q_idx.device)
-    c, s, q = cache.ctype(), seqs.ctype(), queries.ctype()
+    c, s, q = cache.index_ctype(), seqs.ctype(), queries.ctype()
     _lib.check("dsa_index_score_i64", lib.dsa_index_score_i64(
         ctypes.byref(c), ctypes.byref(s), ctypes.byref(q), _ptr(q_idx), _ptr(w), q_idx.shape[1], _ptr(scores),
         _ptr(dev_err), _stream(stream)))
@@ -199,7 +394,7 @@ def index_score_fp8(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, q_
     if scores is None:
         scores = torch.empty((queries.total_q, seqs.block_table.shape[1]), dtype=torch.int64,
                              device=q_idx_e4m3.device)
-    c, s, q = cache.ctype(), seqs.ctype(), queries.ctype()
+    c, s, q = cache.index_ctype(), seqs.ctype(), queries.ctype()
     _lib.check("dsa_index_score_fp8", lib.dsa_index_score_fp8(
         ctypes.byref(c), ctypes.byref(s), ctypes.byref(q), _ptr(q_idx_e4m3), _ptr(w), q_idx_e4m3.shape[1],
         int(w_abs_max), _ptr(scores), _ptr(dev_err), _stream(stream)))
@@ -245,7 +440,7 @@ def select_blocks(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, q_id
         cnt = torch.empty((T,), dtype=torch.int32, device=dev)
     if workspace is None:
         workspace = torch.zeros(select_workspace_size(T), dtype=torch.uint8, device=dev)
-    c, s, q = cache.ctype(), seqs.ctype(), queries.ctype()
+    c, s, q = cache.index_ctype(), seqs.ctype(), queries.ctype()
     _lib.check("dsa_select_blocks", lib.dsa_select_blocks(
         ctypes.byref(c), ctypes.byref(s), ctypes.byref(q), _ptr(q_idx), _ptr(w), q_idx.shape[1], int(w_abs_max),
         _ptr(k_per_seq), int(k_max), _ptr(sel), _ptr(cnt), _ptr(workspace), workspace.numel(), _ptr(dev_err),
@@ -346,6 +541,57 @@ def sparse_attn_prefill(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch
     scale = 1.0 / math.sqrt(q.shape[2]) if sm_scale is None else float(sm_scale)
     c, s, qq = cache.ctype(), seqs.ctype(), queries.ctype()
     _lib.check("dsa_sparse_attn_prefill", lib.dsa_sparse_attn_prefill(
+        ctypes.byref(c), ctypes.byref(s), ctypes.byref(qq), _ptr(q), q.shape[1], _ptr(sel), _ptr(cnt),
+        sel.shape[1], scale, _ptr(out), _ptr(lse), _ptr(dev_err), _stream(stream)))
+    return out, lse
+
+
+def _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, dev_err):
+    if not isinstance(cache, PagedKVCacheFP8):
+        raise TypeError("the fp8 attention calls read a PagedKVCacheFP8")
+    _expect(q, torch.bfloat16, "q")
+    _expect(sel, torch.int32, "sel")
+    _expect(cnt, torch.int32, "cnt")
+    T = queries.total_q
+    if q.dim() != 3 or q.shape[0] != T or q.shape[2] != HEAD_DIM:
+        raise ValueError(f"q must be [{T}][heads][{HEAD_DIM}], got {list(q.shape)}")
+    if sel.dim() != 2 or sel.shape[0] != T or cnt.numel() != T:
+        raise ValueError(f"sel must be [{T}][k_max] and cnt [{T}]")
+    out, lse = _attn_out(q, out, lse)
+    _expect(out, torch.bfloat16, "out")
+    _expect(lse, torch.float32, "lse")
+    if out.shape != q.shape or lse.shape != q.shape[:2]:
+        raise ValueError("out must have q's shape and lse its first two dimensions")
+    _same_device(cache.k_pool, cache.v_pool, cache.k_scale, cache.v_scale, seqs.block_table, seqs.seq_lens,
+                 queries.cu_q, queries.q_pos, q, sel, cnt, out, lse, dev_err)
+    return out, lse, 1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else float(sm_scale)
+
+
+def sparse_attn_decode_fp8(cache: PagedKVCacheFP8, seqs: SeqBatch, queries: QueryBatch, q: torch.Tensor,
+                           sel: torch.Tensor, cnt: torch.Tensor, sm_scale: Optional[float] = None, out=None, lse=None,
+                           workspace: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
+                           stream=None):
+    """sparse_attn_decode over the 8-bit cache: (out bf16, lse fp32), same workspace."""
+    out, lse, scale = _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, dev_err)
+    if workspace is None:
+        workspace = torch.zeros(decode_workspace_size(queries.total_q, q.shape[1], cache.num_kv_heads, sel.shape[1]),
+                                dtype=torch.uint8, device=q.device)
+    _same_device(q, workspace)
+    c, s, qq = cache.ctype(), seqs.ctype(), queries.ctype()
+    _lib.check("dsa_sparse_attn_decode_fp8", load().dsa_sparse_attn_decode_fp8(
+        ctypes.byref(c), ctypes.byref(s), ctypes.byref(qq), _ptr(q), q.shape[1], _ptr(sel), _ptr(cnt),
+        sel.shape[1], scale, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(dev_err), _stream(stream)))
+    return out, lse
+
+
+def sparse_attn_prefill_fp8(cache: PagedKVCacheFP8, seqs: SeqBatch, queries: QueryBatch, q: torch.Tensor,
+                            sel: torch.Tensor, cnt: torch.Tensor, sm_scale: Optional[float] = None, out=None,
+                            lse=None, dev_err: Optional[torch.Tensor] = None, stream=None):
+    """sparse_attn_prefill over the 8-bit cache: (out bf16, lse fp32)."""
+    out, lse, scale = _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, dev_err)
+    c, s, qq = cache.ctype(), seqs.ctype(), queries.ctype()
+    _lib.check("dsa_sparse_attn_prefill_fp8", load().dsa_sparse_attn_prefill_fp8(
         ctypes.byref(c), ctypes.byref(s), ctypes.byref(qq), _ptr(q), q.shape[1], _ptr(sel), _ptr(cnt),
         sel.shape[1], scale, _ptr(out), _ptr(lse), _ptr(dev_err), _stream(stream)))
     return out, lse
@@ -539,9 +785,10 @@ def _rotate(r):
     return n, dst, src, nb
 
 
-def step(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, *, k_new, v_new, kc_new, q, q_idx, w,
+def step(cache, seqs: SeqBatch, queries: QueryBatch, *, k_new, v_new, kc_new, q, q_idx, w,
          k_per_seq, k_max: int, w_abs_max: int = 16, decode: bool = True, fused_select: bool = False,
-         overlap_append: bool = False, fused_decode: bool = False, bufs: Optional[dict] = None,
+         overlap_append: bool = False, fused_decode: bool = False, rope: Optional[Rotary] = None,
+         pos: Optional[torch.Tensor] = None, bufs: Optional[dict] = None,
          dev_err: Optional[torch.Tensor] = None, stream=None):
     """One pass of the hot path: append -> index_score -> topk_blocks -> attention
     (with ``fused_select`` the middle two are the single select_blocks call;
@@ -549,10 +796,20 @@ def step(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, *, k_new, v_n
     as select_blocks_append, overlapping the selection; with ``fused_decode``
     the whole decode step is one decode_fused launch).
 
+    ``cache`` is a PagedKVCache or a PagedKVCacheFP8.  With ``rope`` (a Rotary)
+    the append rotates k_new and q (``pos``: int32 [num_axes][total_q] positions,
+    by default the tokens' places); the rotated queries are in bufs["q_rot"].
+    The overlapped append and the single-launch step take neither.
+
     ``bufs`` (optional, reused across calls) holds the scores / sel / cnt /
     out / lse / workspace tensors; missing ones are allocated.  Returns bufs.
     """
     b = {} if bufs is None else bufs
+    fp8 = isinstance(cache, PagedKVCacheFP8)
+    if (fp8 or rope is not None) and (overlap_append or fused_decode):
+        raise ValueError("overlap_append and fused_decode take a PagedKVCache and rows that are rotated already")
+    if pos is not None and rope is None:
+        raise ValueError("pos needs rope")
     T, dev = queries.total_q, q.device
     if "scores" not in b:
         b["scores"] = torch.empty((T, seqs.block_table.shape[1]), dtype=torch.int32, device=dev)
@@ -581,7 +838,17 @@ def step(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, *, k_new, v_n
         sparse_attn_decode(cache, seqs, queries, q, b["sel"], b["cnt"], out=b["out"], lse=b["lse"],
                            workspace=b["workspace"], dev_err=dev_err, stream=stream)
         return b
-    kv_append(cache, seqs, queries.cu_q, k_new, v_new, kc_new, dev_err=dev_err, stream=stream)
+    if rope is not None:
+        if "q_rot" not in b:
+            b["q_rot"] = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        (kv_append_fp8 if fp8 else kv_append_rope)(
+            cache, seqs, queries.cu_q, k_new, v_new, kc_new, rope, pos_new=pos, queries=queries, q=q, pos_q=pos,
+            q_out=b["q_rot"], dev_err=dev_err, stream=stream)
+        q = b["q_rot"]
+    elif fp8:
+        kv_append_fp8(cache, seqs, queries.cu_q, k_new, v_new, kc_new, dev_err=dev_err, stream=stream)
+    else:
+        kv_append(cache, seqs, queries.cu_q, k_new, v_new, kc_new, dev_err=dev_err, stream=stream)
     if fused_select:
         select_blocks(cache, seqs, queries, q_idx, w, k_per_seq, k_max, w_abs_max, sel=b["sel"], cnt=b["cnt"],
                       workspace=b["select_ws"], dev_err=dev_err, stream=stream)
@@ -591,9 +858,10 @@ def step(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, *, k_new, v_n
         topk_blocks(seqs, queries, b["scores"], k_per_seq, k_max, sel=b["sel"], cnt=b["cnt"], dev_err=dev_err,
                     stream=stream, block_size=cache.block_size)
     if decode:
-        sparse_attn_decode(cache, seqs, queries, q, b["sel"], b["cnt"], out=b["out"], lse=b["lse"],
-                           workspace=b["workspace"], dev_err=dev_err, stream=stream)
+        attend = sparse_attn_decode_fp8 if fp8 else sparse_attn_decode
+        attend(cache, seqs, queries, q, b["sel"], b["cnt"], out=b["out"], lse=b["lse"], workspace=b["workspace"],
+               dev_err=dev_err, stream=stream)
     else:
-        sparse_attn_prefill(cache, seqs, queries, q, b["sel"], b["cnt"], out=b["out"], lse=b["lse"],
-                            dev_err=dev_err, stream=stream)
+        attend = sparse_attn_prefill_fp8 if fp8 else sparse_attn_prefill
+        attend(cache, seqs, queries, q, b["sel"], b["cnt"], out=b["out"], lse=b["lse"], dev_err=dev_err, stream=stream)
     return b

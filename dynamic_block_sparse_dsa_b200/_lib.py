@@ -36,10 +36,34 @@ class QueriesC(ctypes.Structure):
     _fields_ = [("cu_q", c_vp), ("q_pos", c_vp), ("total_q", c_i32)]
 
 
+class KvCacheFp8C(ctypes.Structure):
+    _fields_ = [("k_pool", c_vp), ("v_pool", c_vp), ("kc_pool", c_vp), ("k_scale", c_vp), ("v_scale", c_vp),
+                ("num_pages", c_i32), ("block_size", c_i32), ("num_kv_heads", c_i32), ("head_dim", c_i32),
+                ("idx_dim", c_i32)]
+
+
+class RopeC(ctypes.Structure):
+    _fields_ = [("inv_freq", c_vp), ("pair_axis", c_vp), ("rotary_dim", c_i32), ("layout", c_i32),
+                ("num_axes", c_i32), ("scale", ctypes.c_float)]
+
+
+class NewTokensC(ctypes.Structure):
+    _fields_ = [("cu_new", c_vp), ("total_new", c_i32), ("k", c_vp), ("v", c_vp), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("kc", c_vp), ("pos", c_vp)]
+
+
+class QueryRowsC(ctypes.Structure):
+    _fields_ = [("q", c_vp), ("q_stride", ctypes.c_int64), ("num_heads", c_i32), ("pos", c_vp), ("out", c_vp)]
+
+
 # exported symbol -> (argtypes, restype); mirrors include/dsa.h
 P = ctypes.POINTER
 SIGNATURES = {
     "dsa_kv_append": ([P(KvCacheC), P(SeqsC), c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp], c_i32),
+    "dsa_kv_append_rope": ([P(KvCacheC), P(SeqsC), P(NewTokensC), P(RopeC), P(QueriesC), P(QueryRowsC), c_vp, c_vp],
+                           c_i32),
+    "dsa_kv_append_fp8": ([P(KvCacheFp8C), P(SeqsC), P(NewTokensC), P(RopeC), P(QueriesC), P(QueryRowsC), c_vp, c_vp],
+                          c_i32),
     "dsa_index_score": ([P(KvCacheC), P(SeqsC), P(QueriesC), c_vp, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp],
                         c_i32),
     "dsa_topk_blocks": ([P(SeqsC), P(QueriesC), c_vp, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp], c_i32),
@@ -59,6 +83,10 @@ SIGNATURES = {
                                  ctypes.c_float, c_vp, c_vp, c_vp, c_vp], c_i32),
     "dsa_sparse_attn_decode_noalloc": ([P(KvCacheC), P(SeqsC), P(QueriesC), c_vp, c_i32, c_vp, c_vp, c_i32,
                                         ctypes.c_float, c_vp, c_vp, c_vp, c_vp], c_i32),
+    "dsa_sparse_attn_decode_fp8": ([P(KvCacheFp8C), P(SeqsC), P(QueriesC), c_vp, c_i32, c_vp, c_vp, c_i32,
+                                    ctypes.c_float, c_vp, c_vp, c_vp, ctypes.c_size_t, c_vp, c_vp], c_i32),
+    "dsa_sparse_attn_prefill_fp8": ([P(KvCacheFp8C), P(SeqsC), P(QueriesC), c_vp, c_i32, c_vp, c_vp, c_i32,
+                                     ctypes.c_float, c_vp, c_vp, c_vp, c_vp], c_i32),
     "dsa_decode_fused_workspace_size": ([c_i32, c_i32, c_i32, c_i32], ctypes.c_size_t),
     "dsa_decode_fused": ([P(KvCacheC), P(SeqsC), P(QueriesC), c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32,
                           c_i32, c_vp, c_i32, c_vp, c_i32, ctypes.c_float, c_vp, c_vp, c_vp, c_vp, c_vp,

@@ -27,6 +27,17 @@ int check_cache(const dsa_kv_cache *c) {
     return DSA_OK;
 }
 
+int check_cache_fp8(const dsa_kv_cache_fp8 *c) {
+    if (!c || !c->k_pool || !c->v_pool || !c->kc_pool || !c->k_scale || !c->v_scale) return DSA_ERR_INVALID_ARG;
+    if (!aligned16(c->k_pool) || !aligned16(c->v_pool) || !aligned16(c->kc_pool) || !aligned16(c->k_scale) ||
+        !aligned16(c->v_scale))
+        return DSA_ERR_INVALID_ARG;
+    if (c->num_pages < 1 || c->num_kv_heads < 1) return DSA_ERR_INVALID_ARG;
+    if (block_shift_of(c->block_size) < 0 || c->head_dim != kHeadDim || c->idx_dim != kIdxDim)
+        return DSA_ERR_UNSUPPORTED;
+    return DSA_OK;
+}
+
 int check_seqs(const dsa_seqs *s) {
     if (!s || !s->block_table || !s->seq_lens) return DSA_ERR_INVALID_ARG;
     if (s->num_seqs < 1 || s->max_blocks < 1) return DSA_ERR_INVALID_ARG;
@@ -126,11 +137,13 @@ void attn_schedule(AttnArgs &a, bool allow_split, bool allow_cluster = false) {
     a.interleave = (a.pair_aligned && a.num_kv_heads > 1) ? 1 : 0;
 }
 
-int attn_common(const dsa_kv_cache *cache, const dsa_seqs *seqs, const dsa_queries *queries,
-                const void *q, int32_t num_q_heads, const int32_t *sel, const int32_t *cnt,
-                int32_t k_max, float sm_scale, void *out, float *lse, int32_t *dev_err, AttnArgs &a) {
+// Cache: dsa_kv_cache or dsa_kv_cache_fp8, already checked (the caller sets the scales)
+template <typename Cache>
+int attn_args(const Cache *cache, const dsa_seqs *seqs, const dsa_queries *queries, const void *q,
+              int32_t num_q_heads, const int32_t *sel, const int32_t *cnt, int32_t k_max, float sm_scale,
+              void *out, float *lse, int32_t *dev_err, AttnArgs &a) {
     int rc;
-    if ((rc = check_cache(cache)) || (rc = check_seqs(seqs)) || (rc = check_queries(queries))) return rc;
+    if ((rc = check_seqs(seqs)) || (rc = check_queries(queries))) return rc;
     if (queries->total_q > 0 && (!q || !sel || !cnt || !out)) return DSA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned16(sel)) return DSA_ERR_INVALID_ARG;
     if (k_max < 1 || num_q_heads < 1) return DSA_ERR_INVALID_ARG;
@@ -148,8 +161,8 @@ int attn_common(const dsa_kv_cache *cache, const dsa_seqs *seqs, const dsa_queri
     a = AttnArgs{};
     a.block_shift = bsh;
     a.tile_shift = bsh - 6;
-    a.k_pool = static_cast<const __nv_bfloat16 *>(cache->k_pool);
-    a.v_pool = static_cast<const __nv_bfloat16 *>(cache->v_pool);
+    a.k_pool = cache->k_pool;
+    a.v_pool = cache->v_pool;
     a.num_pages = cache->num_pages;
     a.num_kv_heads = cache->num_kv_heads;
     a.block_table = seqs->block_table;
@@ -169,6 +182,101 @@ int attn_common(const dsa_kv_cache *cache, const dsa_seqs *seqs, const dsa_queri
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.lse = lse;
     a.dev_err = dev_err;
+    return DSA_OK;
+}
+
+int attn_common(const dsa_kv_cache *cache, const dsa_seqs *seqs, const dsa_queries *queries,
+                const void *q, int32_t num_q_heads, const int32_t *sel, const int32_t *cnt,
+                int32_t k_max, float sm_scale, void *out, float *lse, int32_t *dev_err, AttnArgs &a) {
+    const int rc = check_cache(cache);
+    return rc ? rc : attn_args(cache, seqs, queries, q, num_q_heads, sel, cnt, k_max, sm_scale, out, lse, dev_err, a);
+}
+
+int attn_common_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *seqs, const dsa_queries *queries,
+                    const void *q, int32_t num_q_heads, const int32_t *sel, const int32_t *cnt,
+                    int32_t k_max, float sm_scale, void *out, float *lse, int32_t *dev_err, AttnArgs &a) {
+    int rc = check_cache_fp8(cache);
+    if (!rc) rc = attn_args(cache, seqs, queries, q, num_q_heads, sel, cnt, k_max, sm_scale, out, lse, dev_err, a);
+    if (rc) return rc;
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+    return DSA_OK;
+}
+
+// a token stride that holds `heads` rows and keeps every row 16-byte aligned
+bool row_stride_ok(int64_t stride, int32_t heads) { return stride >= (int64_t)heads * kHeadDim && stride % 8 == 0; }
+
+int check_rope(const dsa_rope *r) {
+    if (!r->inv_freq || (r->num_axes > 1 && !r->pair_axis)) return DSA_ERR_INVALID_ARG;
+    if (r->rotary_dim < 1 || r->rotary_dim > kHeadDim || r->num_axes < 1) return DSA_ERR_INVALID_ARG;
+    if (r->layout != DSA_ROPE_HALVES && r->layout != DSA_ROPE_PAIRS) return DSA_ERR_INVALID_ARG;
+    if (!(r->scale - r->scale == 0.f)) return DSA_ERR_INVALID_ARG;   // finite
+    if (r->rotary_dim % 16 != 0 || r->num_axes > 4) return DSA_ERR_UNSUPPORTED;
+    return DSA_OK;
+}
+
+// the arguments of the rotating appends behind the cache: new rows, rotation, query rows
+template <typename Cache>
+int append_rope_args(const Cache *cache, const dsa_seqs *seqs, const dsa_new_tokens *fresh, const dsa_rope *rope,
+                     const dsa_queries *queries, const dsa_query_rows *rows, int32_t *dev_err, AppendRopeArgs &a) {
+    int rc;
+    if ((rc = check_seqs(seqs))) return rc;
+    if (!fresh || fresh->total_new < 0) return DSA_ERR_INVALID_ARG;
+    a = AppendRopeArgs{};
+    if (rope) {
+        if ((rc = check_rope(rope))) return rc;
+        a.rope.inv_freq = rope->inv_freq;
+        a.rope.pair_axis = rope->num_axes > 1 ? rope->pair_axis : nullptr;
+        a.rope.rotary_dim = rope->rotary_dim;
+        a.rope.interleaved = rope->layout == DSA_ROPE_PAIRS;
+        a.rope.num_axes = rope->num_axes;
+        a.rope.scale = rope->scale;
+    }
+    if (fresh->total_new > 0) {
+        if (!fresh->cu_new || !fresh->k || !fresh->v) return DSA_ERR_INVALID_ARG;
+        if (!aligned16(fresh->k) || !aligned16(fresh->v) || (fresh->kc && !aligned16(fresh->kc)))
+            return DSA_ERR_INVALID_ARG;
+        if (!row_stride_ok(fresh->k_stride, cache->num_kv_heads) || !row_stride_ok(fresh->v_stride, cache->num_kv_heads))
+            return DSA_ERR_INVALID_ARG;
+    }
+    if (rows) {
+        if (!rope) return DSA_ERR_INVALID_ARG;   // nothing to do to the queries
+        if ((rc = check_queries(queries))) return rc;
+        if (rows->num_heads < 1) return DSA_ERR_INVALID_ARG;
+        if (queries->total_q > 0 &&
+            (!rows->q || !rows->out || !aligned16(rows->q) || !aligned16(rows->out) ||
+             !row_stride_ok(rows->q_stride, rows->num_heads)))
+            return DSA_ERR_INVALID_ARG;
+        // in place only as a whole: row t of the output is row t of the input
+        if (rows->q == rows->out && rows->q_stride != (int64_t)rows->num_heads * kHeadDim) return DSA_ERR_INVALID_ARG;
+        a.q = static_cast<const __nv_bfloat16 *>(rows->q);
+        a.q_stride = rows->q_stride;
+        a.total_q = queries->total_q;
+        a.num_q_heads = rows->num_heads;
+        a.q_pos = queries->q_pos;
+        a.pos_q = rows->pos;
+        a.q_out = static_cast<__nv_bfloat16 *>(rows->out);
+    }
+    KvAppendArgs &k = a.kv;
+    k.block_shift = block_shift_of(cache->block_size);
+    k.k_pool = cache->k_pool;
+    k.v_pool = cache->v_pool;
+    k.kc_pool = cache->kc_pool;
+    k.num_pages = cache->num_pages;
+    k.num_kv_heads = cache->num_kv_heads;
+    k.block_table = seqs->block_table;
+    k.max_blocks = seqs->max_blocks;
+    k.seq_lens = seqs->seq_lens;
+    k.num_seqs = seqs->num_seqs;
+    k.cu_new = fresh->cu_new;
+    k.total_new = fresh->total_new;
+    k.k_new = fresh->k;
+    k.v_new = fresh->v;
+    k.kc_new = fresh->kc;
+    k.dev_err = dev_err;
+    a.k_stride = fresh->k_stride;
+    a.v_stride = fresh->v_stride;
+    a.pos_new = fresh->pos;
     return DSA_OK;
 }
 
@@ -560,6 +668,64 @@ int dsa_sparse_attn_prefill(const dsa_kv_cache *cache, const dsa_seqs *seqs, con
                             dsa_stream_t stream) {
     AttnArgs a;
     int rc = attn_common(cache, seqs, queries, q, num_q_heads, sel, cnt, k_max, sm_scale, out, lse, dev_err, a);
+    if (rc) return rc;
+    if (queries->total_q == 0) return DSA_OK;
+    attn_schedule(a, false);   // whole pairs per CTA: no partial states, no workspace
+    return from_cuda(launch_sparse_attn(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dsa_kv_append_rope(const dsa_kv_cache *cache, const dsa_seqs *seqs, const dsa_new_tokens *fresh,
+                       const dsa_rope *rope, const dsa_queries *queries, const dsa_query_rows *rows,
+                       int32_t *dev_err, dsa_stream_t stream) {
+    AppendRopeArgs a;
+    int rc = check_cache(cache);
+    if (!rc && !rope) rc = DSA_ERR_INVALID_ARG;
+    if (!rc) rc = append_rope_args(cache, seqs, fresh, rope, queries, rows, dev_err, a);
+    return rc ? rc : from_cuda(launch_kv_append_rope(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dsa_kv_append_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *seqs, const dsa_new_tokens *fresh,
+                      const dsa_rope *rope, const dsa_queries *queries, const dsa_query_rows *rows,
+                      int32_t *dev_err, dsa_stream_t stream) {
+    AppendRopeArgs a;
+    int rc = check_cache_fp8(cache);
+    if (!rc) rc = append_rope_args(cache, seqs, fresh, rope, queries, rows, dev_err, a);
+    if (rc) return rc;
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+    // a CTA of a decode batch takes all heads of its tile (one new row each); a
+    // full tile is 64 rows per head already
+    const bool few = a.kv.total_new <= 4ll * a.kv.num_seqs;
+    a.heads_per_cta = few ? a.kv.num_kv_heads : 1;
+    const long long tiles = append_fp8_tile_ctas(a.kv.total_new, a.kv.num_seqs, a.kv.num_kv_heads, a.heads_per_cta);
+    if (tiles + a.total_q >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
+    a.tile_ctas = (int)tiles;
+    return from_cuda(launch_kv_append_fp8(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dsa_sparse_attn_decode_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *seqs, const dsa_queries *queries,
+                               const void *q, int32_t num_q_heads, const int32_t *sel, const int32_t *cnt,
+                               int32_t k_max, float sm_scale, void *out, float *lse, void *workspace,
+                               size_t workspace_bytes, int32_t *dev_err, dsa_stream_t stream) {
+    AttnArgs a;
+    int rc = attn_common_fp8(cache, seqs, queries, q, num_q_heads, sel, cnt, k_max, sm_scale, out, lse, dev_err, a);
+    if (rc) return rc;
+    if (queries->total_q == 0) return DSA_OK;
+    const DecodeLayout L = decode_layout(queries->total_q, num_q_heads, cache->num_kv_heads);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < L.total) return DSA_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    a.counters = reinterpret_cast<int32_t *>(ws + L.counters);
+    a.part = reinterpret_cast<float *>(ws + L.part);
+    attn_schedule(a, true, true);
+    return from_cuda(launch_sparse_attn(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dsa_sparse_attn_prefill_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *seqs, const dsa_queries *queries,
+                                const void *q, int32_t num_q_heads, const int32_t *sel, const int32_t *cnt,
+                                int32_t k_max, float sm_scale, void *out, float *lse, int32_t *dev_err,
+                                dsa_stream_t stream) {
+    AttnArgs a;
+    int rc = attn_common_fp8(cache, seqs, queries, q, num_q_heads, sel, cnt, k_max, sm_scale, out, lse, dev_err, a);
     if (rc) return rc;
     if (queries->total_q == 0) return DSA_OK;
     attn_schedule(a, false);   // whole pairs per CTA: no partial states, no workspace

@@ -43,6 +43,33 @@ struct KvAppendArgs {
     int overlap_prev;
 };
 
+// rotation of keys and queries by position (rotary_dim 0: none)
+struct RopeArgs {
+    const float *inv_freq;      // [rotary_dim / 2] radians per position
+    const int32_t *pair_axis;   // [rotary_dim / 2] axis of each pair, or null (axis 0)
+    int rotary_dim, interleaved, num_axes;
+    float scale;
+};
+
+// append with rotation and rotated queries; kv.k_pool / kv.v_pool hold bf16 rows,
+// or E4M3 codes with their scales
+struct AppendRopeArgs {
+    KvAppendArgs kv;
+    long long k_stride, v_stride;   // elements between tokens of kv.k_new / kv.v_new
+    const int32_t *pos_new;         // [num_axes][total_new], or null: the cache position
+    RopeArgs rope;
+    const __nv_bfloat16 *q;         // [total_q][num_q_heads][128], q_stride elements between queries
+    long long q_stride;
+    int total_q, num_q_heads;
+    const int32_t *q_pos;           // [total_q]
+    const int32_t *pos_q;           // [num_axes][total_q], or null: q_pos
+    __nv_bfloat16 *q_out;           // [total_q][num_q_heads][128]
+    // E4M3 cache only
+    float *k_scale, *v_scale;       // [num_pages][block_size / 64][num_kv_heads]
+    int heads_per_cta;              // KV heads per append CTA
+    int tile_ctas;                  // append CTAs (the query CTAs come after them)
+};
+
 struct IndexScoreArgs {
     const int8_t *kc_pool;
     int num_pages;
@@ -113,7 +140,8 @@ struct SelectArgs {
 };
 
 struct AttnArgs {
-    const __nv_bfloat16 *k_pool, *v_pool;
+    const void *k_pool, *v_pool;   // bf16, or E4M3 codes when the scales are given
+    const float *k_scale, *v_scale;   // E4M3 cache: [num_pages][block_size / 64][num_kv_heads], else null
     int num_pages, num_kv_heads;
     // tokens per KV block = 1 << block_shift; the kernel works in 64-token
     // tiles, tile_shift = block_shift - 6 of them per block
@@ -181,6 +209,10 @@ struct FusedArgs {
 };
 
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t stream);
+cudaError_t launch_kv_append_rope(const AppendRopeArgs &a, cudaStream_t stream);
+cudaError_t launch_kv_append_fp8(const AppendRopeArgs &a, cudaStream_t stream);
+// append CTAs of launch_kv_append_fp8 (the host checks that the grid is in range)
+long long append_fp8_tile_ctas(int total_new, int num_seqs, int num_kv_heads, int heads_per_cta);
 cudaError_t launch_index_score(const IndexScoreArgs &a, cudaStream_t stream);
 // tensor-core (tcgen05 int8) scoring for batches with many queries per sequence
 cudaError_t launch_index_score_tc(const IndexScoreArgs &a, int num_sms, cudaStream_t stream);

@@ -1,0 +1,485 @@
+// kv_append_rope.cu -- appending new tokens with the position rotation applied
+// on the way, into the bf16 cache and into the 8-bit (E4M3) cache.
+//
+// "Day-0 Readiness for Trillion-Parameter Models: Engineering Sparse Attention
+// and Expert Weight Compression", section "KV Cache Layout": prefill writes
+// blocks in batch, decode appends one token, both through one block table.
+// The rotation and the 8-bit storage have no counterpart on the pages.
+//
+// Rotation.  Pair i of a row at position p turns by the angle p * inv_freq[i]:
+//     (x, y) -> (x cos - y sin, y cos + x sin) * scale.
+// At a million tokens p * inv_freq in fp32 is off by up to 0.06 rad, so the
+// angle is kept in turns as a 64-bit fraction: f = inv_freq / (2 pi) mod 1
+// times 2^64, and p * f mod 2^64 is the fraction of a turn, exact but for the
+// rounding of f (2^-53 of a turn per position).  Its upper 32 bits go through
+// sincospif.  The rotation itself is fp32, rounded once to the stored type.
+//
+// E4M3 cache.  A tile is 64 tokens of a block; each (tile, KV head) has one
+// scale for K and one for V, a power of two when written here:
+//     need = the least 2^e, e >= -100, with max |x| <= 448 * 2^e over the new rows
+//     s'   = need for a tile whose first token is new, else max(s, need)
+//     new rows: e4m3(x / s');  rows held from before: e4m3(code * s / s') if s' != s.
+// A power of two keeps the 4-bit significand of every code that stays normal,
+// so growing the scale again and again does not add up roundings; a scale of
+// max/448 would spread the codes by up to 2x more evenly but re-round each.
+#include "dsa_kernels.h"
+
+#include <cuda_fp8.h>
+#include <float.h>
+
+namespace dsa {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kSlots = kThreads / 8;   // rows in flight per pass: eight threads (32 bytes each) per row
+constexpr int kPairs = kHeadDim / 2;
+constexpr int kMinScaleExp = -100;
+
+// the fraction of a turn per position as a 64-bit fixed-point number
+__device__ __forceinline__ unsigned long long turns_q64(float inv_freq) {
+    double f = (double)inv_freq * 0.15915494309189535;   // 1 / (2 pi)
+    f -= floor(f);
+    return (unsigned long long)(f * 18446744073709551616.0);
+}
+
+// (cos, sin) of the angle at position p, times the rotation's scale
+__device__ __forceinline__ float2 rope_cs(int p, unsigned long long f, float scale) {
+    const int hi = (int)(((unsigned long long)(long long)p * f) >> 32);
+    float s, c;
+    sincospif((float)hi * 0x1p-31f, &s, &c);
+    return make_float2(c * scale, s * scale);
+}
+
+// the (cos, sin) table of one row: thread j of the row owns pairs 8j..8j+7,
+// kept as [pair of pairs m][j] so that the eight threads' 16-byte reads are
+// free of bank conflicts
+struct RopeTab {
+    float4 cs[4][8];
+};
+__device__ __forceinline__ void put_cs(RopeTab &t, int pair, float2 cs) {
+    reinterpret_cast<float2 *>(&t.cs[(pair >> 1) & 3][pair >> 3])[pair & 1] = cs;
+}
+
+// 16-byte chunks (8 dims each) of a row that thread j owns.  Rotated threads
+// (j < rotary_dim / 16) own both halves of eight pairs: chunks j and
+// j + rotary_dim / 16 when a pair is (i, i + rotary_dim / 2), adjacent chunks
+// when it is (2i, 2i + 1); the others own two chunks that are only copied.
+__device__ __forceinline__ void own_chunks(const RopeArgs &r, int j, int &c0, int &c1) {
+    const bool halves = !r.interleaved && j < (r.rotary_dim >> 4);
+    c0 = halves ? j : 2 * j;
+    c1 = halves ? j + (r.rotary_dim >> 4) : 2 * j + 1;
+}
+
+__device__ __forceinline__ void unpack8(const uint4 &u, float *x) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x[2 * k] = __uint_as_float(w[k] << 16);
+        x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float *x) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                      pack_bf16x2(x[6], x[7]));
+}
+
+// rotate the sixteen values of thread j (chunk c0, then chunk c1)
+__device__ __forceinline__ void rotate16(float *x, const RopeTab &t, int j, int interleaved) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const float4 cs = t.cs[m][j];
+        const float cc[2] = {cs.x, cs.z}, ss[2] = {cs.y, cs.w};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int e = 2 * m + k;   // both layouts by constant indexes, so that x stays in registers
+            if (interleaved) {
+                const float u = x[2 * e], v = x[2 * e + 1];
+                x[2 * e] = u * cc[k] - v * ss[k];
+                x[2 * e + 1] = v * cc[k] + u * ss[k];
+            } else {
+                const float u = x[e], v = x[8 + e];
+                x[e] = u * cc[k] - v * ss[k];
+                x[8 + e] = v * cc[k] + u * ss[k];
+            }
+        }
+    }
+}
+
+// Last index s in [0, n) whose value is <= i (values ascend), by one warp: 32
+// independent loads per step while n is small, a binary search beyond that.
+template <typename F>
+__device__ __forceinline__ int last_le_warp(int n, int i, F value) {
+    if (n <= 256) {
+        int count = 0;
+        for (int b = 0; b < n; b += 32) {
+            const int s = b + (int)(threadIdx.x & 31);
+            count += __popc(__ballot_sync(0xffffffffu, s < n && value(s) <= i));
+        }
+        return max(count - 1, 0);
+    }
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (value(mid) <= i) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// position of row i on the axis of `pair`
+__device__ __forceinline__ int axis_pos(const RopeArgs &r, const int32_t *pos, int total, int i, int pair,
+                                        int plain, uint32_t &err) {
+    if (!pos) return plain;
+    int axis = r.pair_axis ? __ldg(r.pair_axis + pair) : 0;
+    if (axis < 0 || axis >= r.num_axes) {
+        err |= DSA_DEV_ERR_POS;
+        axis = 0;
+    }
+    return __ldg(pos + (size_t)axis * total + i);
+}
+
+// where a new token lands; page < 0 when it is skipped
+struct Place {
+    int pos, page, slot;
+    bool ends_block;   // the last new token of its block
+};
+__device__ __forceinline__ Place place_of(const KvAppendArgs &a, int i, uint32_t &err) {
+    Place p{0, -1, 0, false};
+    const int s = last_le_warp(a.num_seqs, i, [&](int k) { return __ldg(a.cu_new + k); });
+    const int first = __ldg(a.cu_new + s), last = __ldg(a.cu_new + s + 1);
+    const int len = __ldg(a.seq_lens + s), n = last - first;
+    if (i < first || i >= last || n > len) {
+        err |= DSA_DEV_ERR_POS;
+        return p;
+    }
+    p.pos = len - n + (i - first);
+    const int blk = p.pos >> a.block_shift;
+    p.slot = p.pos & ((1 << a.block_shift) - 1);
+    if (blk >= a.max_blocks) {
+        err |= DSA_DEV_ERR_POS;
+        return p;
+    }
+    p.page = __ldg(a.block_table + (size_t)s * a.max_blocks + blk);
+    if (p.page < 0 || p.page >= a.num_pages) {
+        err |= DSA_DEV_ERR_PAGE;
+        p.page = -1;
+    }
+    p.ends_block = i == last - 1 || p.slot == (1 << a.block_shift) - 1;
+    return p;
+}
+
+// the rotated query rows of one query and, in the bf16 cache, the K and V rows
+// of one new token: row r of the CTA's list is K head r, then V head, then
+// query head.  Loads of kBatch rows per thread are issued before the tables
+// are ready and before the wait for the kernels ahead.
+template <bool kKv>
+__device__ __forceinline__ void token_rows(const AppendRopeArgs &a, int i) {
+    __shared__ RopeTab s_tab[2];   // K, q
+    constexpr int kBatch = 3;
+    const int tid = threadIdx.x, j = tid & 7, slot = tid >> 3;
+    const bool has_new = kKv && i < a.kv.total_new, has_q = i < a.total_q;
+    const int hkv = has_new ? a.kv.num_kv_heads : 0, nq = has_q ? a.num_q_heads : 0;
+    const int rows = 2 * hkv + nq;
+    const RopeArgs &r = a.rope;
+    int c0, c1;
+    own_chunks(r, j, c0, c1);
+    const bool turned = j < (r.rotary_dim >> 4);
+    uint4 lo[kBatch], hi[kBatch];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int row = base + b * kSlots + slot;
+            if (row < rows) {
+                const __nv_bfloat16 *src;
+                if (row < hkv) src = static_cast<const __nv_bfloat16 *>(a.kv.k_new) + i * a.k_stride + row * kHeadDim;
+                else if (row < 2 * hkv) src = static_cast<const __nv_bfloat16 *>(a.kv.v_new) + i * a.v_stride + (row - hkv) * kHeadDim;
+                else src = a.q + i * a.q_stride + (row - 2 * hkv) * kHeadDim;
+                lo[b] = reinterpret_cast<const uint4 *>(src)[c0];
+                hi[b] = reinterpret_cast<const uint4 *>(src)[c1];
+            }
+        }
+    };
+    load(0);
+    uint32_t err = 0;
+    Place p{0, -1, 0, false};
+    if (has_new) p = place_of(a.kv, i, err);
+    if (tid < 2 * kPairs) {
+        const int pair = tid & (kPairs - 1);
+        const bool is_q = tid >= kPairs;
+        if (pair < (r.rotary_dim >> 1) && (is_q ? has_q : has_new)) {
+            const int pos = is_q ? axis_pos(r, a.pos_q, a.total_q, i, pair, a.pos_q ? 0 : __ldg(a.q_pos + i), err)
+                                 : axis_pos(r, a.pos_new, a.kv.total_new, i, pair, p.pos, err);
+            put_cs(s_tab[is_q], pair, rope_cs(pos, turns_q64(__ldg(r.inv_freq + pair)), r.scale));
+        }
+    }
+    if (err) set_err(a.kv.dev_err, err);
+    __syncthreads();
+    pdl_wait();
+    for (int base = 0; base < rows; base += kBatch * kSlots) {
+        if (base) load(base);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int row = base + b * kSlots + slot;
+            if (row >= rows) break;
+            const bool is_q = row >= 2 * hkv, is_v = !is_q && row >= hkv;
+            if (turned && !is_v) {
+                float x[16];
+                unpack8(lo[b], x);
+                unpack8(hi[b], x + 8);
+                rotate16(x, s_tab[is_q], j, r.interleaved);
+                lo[b] = pack8(x);
+                hi[b] = pack8(x + 8);
+            }
+            uint4 *dst;
+            if (is_q) {
+                dst = reinterpret_cast<uint4 *>(a.q_out + ((size_t)i * a.num_q_heads + (row - 2 * hkv)) * kHeadDim);
+            } else {
+                if (p.page < 0) continue;
+                __nv_bfloat16 *pool = static_cast<__nv_bfloat16 *>(is_v ? a.kv.v_pool : a.kv.k_pool);
+                const size_t tok = ((size_t)p.page << a.kv.block_shift) + p.slot;
+                dst = reinterpret_cast<uint4 *>(pool + (tok * hkv + (is_v ? row - hkv : row)) * kHeadDim);
+            }
+            dst[c0] = lo[b];
+            dst[c1] = hi[b];
+        }
+    }
+    if (has_new && a.kv.kc_new && p.page >= 0 && p.ends_block && tid < kIdxDim / 16)
+        reinterpret_cast<uint4 *>(a.kv.kc_pool)[(size_t)p.page * (kIdxDim / 16) + tid] =
+            __ldg(reinterpret_cast<const uint4 *>(a.kv.kc_new) + (size_t)i * (kIdxDim / 16) + tid);
+}
+
+// ------------------------------------------------------------------ E4M3 cache
+
+// least 2^e >= 2^kMinScaleExp with amax <= 448 * 2^e, for a finite amax >= 0:
+// 448 = 1.75 * 2^8, so e is amax's exponent - 8, one more if its significand
+// exceeds 1.75.  (A subnormal amax lands on the floor.)
+__device__ __forceinline__ float scale_for(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return __uint_as_float((uint32_t)(max(e, kMinScaleExp) + 127) << 23);
+}
+
+__device__ __forceinline__ uint2 to_e4m3x8(const float *x, float inv) {
+    uint32_t h[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        h[k] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * k] * inv, x[2 * k + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+__device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float ratio) {
+    float x[4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * k)), __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        x[2 * k] = f.x * ratio;
+        x[2 * k + 1] = f.y * ratio;
+    }
+    const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
+    return a | (b << 16);
+}
+
+constexpr int kRowsPT = 2;                    // rows whose values a thread holds while the maximum forms
+constexpr int kPassRows = kRowsPT * kSlots;   // = 64: a full tile of one head
+
+// One CTA per (tile with new tokens, K or V, group of heads).  A pass takes as
+// many heads as fit 64 rows -- one head of a full tile, all heads of a decode
+// token -- and holds their values in registers between the maximum and the
+// stores, so the new rows are read once.
+__device__ __forceinline__ void tile_rows(const AppendRopeArgs &a, int item) {
+    __shared__ RopeTab s_tab[kBlockSize];
+    __shared__ unsigned long long s_freq[kPairs];
+    __shared__ uint32_t s_amax[kPassRows];
+    __shared__ float s_old[kPassRows], s_new[kPassRows];
+    const KvAppendArgs &kv = a.kv;
+    const RopeArgs &r = a.rope;
+    const int tid = threadIdx.x, j = tid & 7, slot = tid >> 3;
+    const int groups = (kv.num_kv_heads + a.heads_per_cta - 1) / a.heads_per_cta;
+    const bool is_v = (item / groups) & 1;
+    const int h_begin = (item % groups) * a.heads_per_cta;
+    const int h_end = min(h_begin + a.heads_per_cta, kv.num_kv_heads);
+    const int unit = item / (2 * groups);
+    // sequence s owns the units from cu_new[s] / 64 + 2 s on: n tokens lie in
+    // at most n / 64 + 2 tiles, and the next sequence starts no earlier
+    const int s = last_le_warp(kv.num_seqs, unit, [&](int k) { return (__ldg(kv.cu_new + k) >> 6) + 2 * k; });
+    const int first = __ldg(kv.cu_new + s), last = __ldg(kv.cu_new + s + 1), len = __ldg(kv.seq_lens + s);
+    const bool reports = tid == 0 && h_begin == 0 && !is_v;
+    if (unit == 0 && reports && __ldg(kv.cu_new + kv.num_seqs) < kv.total_new) set_err(kv.dev_err, DSA_DEV_ERR_POS);
+    const int n = last - first;
+    if (first < 0 || n < 0 || last > kv.total_new || n > len) {
+        if (reports) set_err(kv.dev_err, DSA_DEV_ERR_POS);
+        return;
+    }
+    const int pos0 = len - n;                                    // first new position
+    const long long t0_wide = ((long long)(pos0 >> 6) + unit - ((first >> 6) + 2 * s)) << 6;
+    if (n == 0 || t0_wide >= len) return;
+    const int t0 = (int)t0_wide;                                 // this tile's first position
+    const int blk = t0 >> kv.block_shift;
+    if (blk >= kv.max_blocks) {
+        if (reports) set_err(kv.dev_err, DSA_DEV_ERR_POS);
+        return;
+    }
+    const int page = __ldg(kv.block_table + (size_t)s * kv.max_blocks + blk);
+    if (page < 0 || page >= kv.num_pages) {
+        if (reports) set_err(kv.dev_err, DSA_DEV_ERR_PAGE);
+        return;
+    }
+    const int held = max(pos0 - t0, 0);                          // slots filled before
+    const int cnt = min(len - t0, kBlockSize) - held;            // new tokens of the tile, 1..64
+    const int i0 = first + (t0 + held - pos0);                   // the first of them
+    const int H = kv.num_kv_heads;
+    const size_t row0 = ((size_t)page << kv.block_shift) + (t0 & ((1 << kv.block_shift) - 1));   // pool row of slot 0
+    uint8_t *pool = static_cast<uint8_t *>(is_v ? kv.v_pool : kv.k_pool) + row0 * H * kHeadDim;
+    float *scales = (is_v ? a.v_scale : a.k_scale) + (row0 >> 6) * H;
+    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(is_v ? kv.v_new : kv.k_new);
+    const long long stride = is_v ? a.v_stride : a.k_stride;
+    const bool rotated = !is_v && r.rotary_dim > 0;
+    const bool turned = rotated && j < (r.rotary_dim >> 4);
+    int c0 = 2 * j, c1 = 2 * j + 1;
+    if (rotated) own_chunks(r, j, c0, c1);
+
+    uint32_t err = 0;
+    if (rotated) {
+        if (tid < (r.rotary_dim >> 1)) s_freq[tid] = turns_q64(__ldg(r.inv_freq + tid));
+        __syncthreads();
+        for (int e = tid; e < cnt * kPairs; e += kThreads) {
+            const int tok = e / kPairs, pair = e % kPairs;
+            if (pair < (r.rotary_dim >> 1)) {
+                const int pos = axis_pos(r, a.pos_new, kv.total_new, i0 + tok, pair, t0 + held + tok, err);
+                put_cs(s_tab[tok], pair, rope_cs(pos, s_freq[pair], r.scale));
+            }
+        }
+    }
+    const int per_pass = min(kPassRows / cnt, h_end - h_begin);   // heads per pass (cnt <= 64)
+    bool waited = false;
+    for (int hb = h_begin; hb < h_end; hb += per_pass) {
+        const int nh = min(per_pass, h_end - hb);
+        float x[kRowsPT][16];
+        if (tid < nh) s_amax[tid] = 0u;
+#pragma unroll
+        for (int k = 0; k < kRowsPT; ++k) {
+            const int row = k * kSlots + slot;
+            if (row < nh * cnt) {
+                const int h = row / cnt, tok = row - h * cnt;
+                const uint4 *p = reinterpret_cast<const uint4 *>(src + (i0 + tok) * stride + (size_t)(hb + h) * kHeadDim);
+                unpack8(p[c0], x[k]);
+                unpack8(p[c1], x[k] + 8);
+            }
+        }
+        if (!waited) {   // the scales and codes held from before, and every store, come after the kernels ahead
+            pdl_wait();
+            waited = true;
+        }
+        if (tid < nh && held > 0) s_old[tid] = ld_ordered_cg(scales + hb + tid);
+        __syncthreads();   // tables, cleared maxima, held scales
+#pragma unroll
+        for (int k = 0; k < kRowsPT; ++k) {
+            const int row = k * kSlots + slot;
+            float m = 0.f;
+            if (row < nh * cnt) {
+                const int tok = row - (row / cnt) * cnt;
+                if (turned) rotate16(x[k], s_tab[tok], j, r.interleaved);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float v = fabsf(x[k][e]);
+                    if (v <= FLT_MAX) m = fmaxf(m, v);
+                    else err |= DSA_DEV_ERR_VALUE;
+                }
+            }
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            // the maximum does not depend on the order (non-negative floats order as their bits)
+            if (j == 0 && row < nh * cnt) atomicMax(&s_amax[row / cnt], __float_as_uint(m));
+        }
+        __syncthreads();
+        if (tid < nh) {
+            const float need = scale_for(__uint_as_float(s_amax[tid]));
+            float now = need;
+            if (held > 0) {
+                const float was = s_old[tid];
+                // a held scale that is not a positive finite number says nothing about its codes
+                const bool good = was > 0.f && was <= FLT_MAX;
+                if (good) now = fmaxf(was, need);
+                else s_old[tid] = now;   // no rescaling
+                if (now != was) scales[hb + tid] = now;
+            } else {
+                scales[hb + tid] = now;
+            }
+            s_new[tid] = now;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kRowsPT; ++k) {
+            const int row = k * kSlots + slot;
+            if (row < nh * cnt) {
+                const int h = row / cnt, tok = row - h * cnt;
+                const float inv = 1.f / s_new[h];
+                uint2 *dst = reinterpret_cast<uint2 *>(pool + ((size_t)(held + tok) * H + hb + h) * kHeadDim);
+                dst[c0] = to_e4m3x8(x[k], inv);
+                dst[c1] = to_e4m3x8(x[k] + 8, inv);
+            }
+        }
+        if (held > 0) {
+            for (int h = 0; h < nh; ++h) {
+                if (s_old[h] == s_new[h]) continue;   // the same for the whole CTA
+                const float ratio = s_old[h] / s_new[h];
+                for (int tok = slot; tok < held; tok += kSlots) {
+                    uint4 *w = reinterpret_cast<uint4 *>(pool + ((size_t)tok * H + hb + h) * kHeadDim) + j;
+                    uint4 c = *w;   // a plain load stays behind the wait
+                    c.x = rescale_e4m3x4(c.x, ratio);
+                    c.y = rescale_e4m3x4(c.y, ratio);
+                    c.z = rescale_e4m3x4(c.z, ratio);
+                    c.w = rescale_e4m3x4(c.w, ratio);
+                    *w = c;
+                }
+            }
+        }
+        __syncthreads();   // the shared words of this pass are free
+    }
+    if (err) set_err(kv.dev_err, err);
+    // the coarse key of the block that the tile's last new token ends
+    const int end = t0 + held + cnt;                             // position behind it
+    const bool ends_block = end == len || (end & ((1 << kv.block_shift) - 1)) == 0;
+    if (!is_v && h_begin == 0 && kv.kc_new && ends_block && tid < kIdxDim / 16)
+        reinterpret_cast<uint4 *>(kv.kc_pool)[(size_t)page * (kIdxDim / 16) + tid] =
+            __ldg(reinterpret_cast<const uint4 *>(kv.kc_new) + (size_t)(i0 + cnt - 1) * (kIdxDim / 16) + tid);
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(AppendRopeArgs a) {
+    pdl_trigger();
+    token_rows<true>(a, blockIdx.x);
+}
+
+__global__ void __launch_bounds__(kThreads) kv_append_fp8_kernel(AppendRopeArgs a) {
+    pdl_trigger();
+    if ((int)blockIdx.x < a.tile_ctas) tile_rows(a, blockIdx.x);
+    else token_rows<false>(a, blockIdx.x - a.tile_ctas);
+    // also where a CTA had nothing to do: whatever waits for this kernel waits
+    // for the kernels ahead of it too
+    pdl_wait();
+}
+
+cudaError_t launch_kv_append_rope(const AppendRopeArgs &a, cudaStream_t stream) {
+    const int ctas = a.kv.total_new > a.total_q ? a.kv.total_new : a.total_q;
+    if (ctas == 0) return cudaSuccess;
+    return launch_pdl(kv_append_rope_kernel, dim3(ctas), dim3(kThreads), 0, stream, a);
+}
+
+long long append_fp8_tile_ctas(int total_new, int num_seqs, int num_kv_heads, int heads_per_cta) {
+    if (total_new == 0) return 0;
+    const long long units = total_new / kBlockSize + 2ll * num_seqs;
+    return units * 2 * ((num_kv_heads + heads_per_cta - 1) / heads_per_cta);
+}
+
+cudaError_t launch_kv_append_fp8(const AppendRopeArgs &a, cudaStream_t stream) {
+    const long long ctas = (long long)a.tile_ctas + a.total_q;
+    if (ctas == 0) return cudaSuccess;
+    return launch_pdl(kv_append_fp8_kernel, dim3((unsigned)ctas), dim3(kThreads), 0, stream, a);
+}
+
+}  // namespace dsa

@@ -39,8 +39,11 @@
  *    predecessor before it reads anything a library call writes (the pools,
  *    scores, selections).  Before that wait a kernel may already read the
  *    batch description and its own inputs (block_table, seq_lens, cu_q, q_pos,
- *    k_per_seq, q_idx, w, q): these must not be outputs of the library call
- *    issued just before it on the same stream.  Work from other kernels is
+ *    k_per_seq, q_idx, w, q, and an append's new rows, positions and rotation):
+ *    these must not be outputs of the library call issued just before it on
+ *    the same stream.  (One exception: the attention calls read their q after
+ *    the wait, so q may come from a dsa_kv_append_rope or dsa_kv_append_fp8
+ *    just before.)  Work from other kernels is
  *    waited for in full, as usual.
  *  - Calls on different streams may run at the same time (independent
  *    batches in flight, one stream each) as long as no call writes what
@@ -87,7 +90,7 @@ enum {
 #define DSA_DEV_ERR_SEL 4u   /* selected block id outside the query's visible blocks */
 #define DSA_DEV_ERR_K 8u     /* k_per_seq[s] outside [1, k_max] */
 #define DSA_DEV_ERR_WAIT 16u /* a bounded in-kernel wait gave up (work of that unit skipped) */
-#define DSA_DEV_ERR_VALUE 32u /* an FP8 input code is NaN (read as 0) */
+#define DSA_DEV_ERR_VALUE 32u /* an FP8 indexer code is NaN (read as 0); a value appended to an FP8 cache is not finite */
 
 typedef struct {
     void *k_pool;          /* bf16 [num_pages][block_size][num_kv_heads][head_dim] */
@@ -130,6 +133,100 @@ typedef struct {
 int dsa_kv_append(const dsa_kv_cache *cache, const dsa_seqs *seqs, const int32_t *cu_new,
                   int32_t total_new, const void *k_new, const void *v_new,
                   const int8_t *kc_new, int32_t *dev_err, dsa_stream_t stream);
+
+/*
+ * Rotary positions.  The pages have no counterpart to this part: the models
+ * that use such a cache rotate keys and queries by position before storing and
+ * attending.  Pair i of a row (i < rotary_dim / 2) at position p becomes
+ *     (x cos a - y sin a, y cos a + x sin a) * scale,   a = p * inv_freq[i],
+ * computed in fp32 from an angle that is exact to 2^-24 of a turn at any int32
+ * position, and rounded once.  Dims from rotary_dim on are copied.
+ *   layout: DSA_ROPE_HALVES pairs dims (i, i + rotary_dim / 2), DSA_ROPE_PAIRS
+ *           dims (2i, 2i + 1).
+ *   rotary_dim: a multiple of 16, 16..128 (others are DSA_ERR_UNSUPPORTED).
+ *   num_axes 1..4: with more than one (time, height, width of images and
+ *           video), pair i turns by the position on axis pair_axis[i].
+ * Positions are int32 [num_axes][tokens], any value; NULL stands for the
+ * token's place in its sequence (q_pos for a query) on every axis.
+ * Device errors: DSA_DEV_ERR_POS for a pair_axis entry outside [0, num_axes)
+ * (axis 0 is used).
+ */
+enum { DSA_ROPE_HALVES = 0, DSA_ROPE_PAIRS = 1 };
+
+typedef struct {
+    const float *inv_freq;     /* [rotary_dim / 2] radians per position */
+    const int32_t *pair_axis;  /* [rotary_dim / 2], or NULL with one axis */
+    int32_t rotary_dim;
+    int32_t layout;            /* DSA_ROPE_HALVES or DSA_ROPE_PAIRS */
+    int32_t num_axes;
+    float scale;               /* finite; 1 for the plain rotation */
+} dsa_rope;
+
+typedef struct {
+    const int32_t *cu_new;     /* [num_seqs + 1], as in dsa_kv_append */
+    int32_t total_new;
+    const void *k, *v;         /* bf16 [total_new][num_kv_heads][128], token strides below */
+    int64_t k_stride, v_stride; /* elements from one token to the next: at least num_kv_heads * 128, multiples of 8 */
+    const int8_t *kc;          /* int8 [total_new][idx_dim] or NULL, as in dsa_kv_append */
+    const int32_t *pos;        /* [num_axes][total_new] or NULL (the cache position) */
+} dsa_new_tokens;
+
+typedef struct {
+    const void *q;             /* bf16 [total_q][num_heads][128], token stride below */
+    int64_t q_stride;          /* elements from one query to the next, as k_stride */
+    int32_t num_heads;
+    const int32_t *pos;        /* [num_axes][total_q] or NULL (q_pos) */
+    void *out;                 /* bf16 [total_q][num_heads][128]; q itself only where q_stride is num_heads * 128 */
+} dsa_query_rows;
+
+/*
+ * dsa_kv_append_rope -- dsa_kv_append with the keys rotated on the way, and
+ * the step's queries rotated in the same launch.  K rows go into the cache
+ * rotated, V rows and coarse keys as they are.  rows NULL: no queries (queries
+ * is not read either); total_new 0: only the queries.
+ * Device errors: those of dsa_kv_append and of the rotation.
+ */
+int dsa_kv_append_rope(const dsa_kv_cache *cache, const dsa_seqs *seqs, const dsa_new_tokens *fresh,
+                       const dsa_rope *rope, const dsa_queries *queries, const dsa_query_rows *rows,
+                       int32_t *dev_err, dsa_stream_t stream);
+
+/*
+ * The 8-bit cache: K and V as FP8 E4M3 codes (OCP 8-bit float, as above) with
+ * one fp32 scale per 64-token tile of a block and KV head; a stored value is
+ * code * scale.  The indexer and selection calls read the coarse keys alone:
+ * give them a dsa_kv_cache with the same kc_pool and sizes.
+ */
+typedef struct {
+    void *k_pool;          /* E4M3 [num_pages][block_size][num_kv_heads][head_dim] */
+    void *v_pool;          /* E4M3, same shape */
+    int8_t *kc_pool;       /* int8 [num_pages][idx_dim] */
+    float *k_scale;        /* [num_pages][block_size / 64][num_kv_heads], 16-byte aligned */
+    float *v_scale;        /* same shape */
+    int32_t num_pages;
+    int32_t block_size;    /* 64, 128, 256 or 512 */
+    int32_t num_kv_heads;
+    int32_t head_dim;      /* 128 */
+    int32_t idx_dim;       /* 64 */
+} dsa_kv_cache_fp8;
+
+/*
+ * dsa_kv_append_fp8 -- dsa_kv_append_rope into the 8-bit cache (rope NULL: the
+ * keys are stored as they are, and rows must be NULL).  For each tile that
+ * gets new tokens, and each KV head, K and V apart:
+ *     need  = the least 2^e, e >= -100, with |x| <= 448 * 2^e for the finite new values x
+ *     scale = need where the tile's first token is new, else max(held scale, need)
+ *     new codes = E4M3(x / scale); held codes = E4M3(code * held scale / scale)
+ * rounded to nearest even, from the fp32 result of the rotation (x times the
+ * fp32 reciprocal of the scale, which is exact for powers of two).  An
+ * infinity is stored as +-448 * scale and a NaN as NaN, each with
+ * DSA_DEV_ERR_VALUE.  A held scale that is not positive and finite is replaced
+ * without touching the codes.  The pages a call appends to belong to one
+ * sequence each.
+ * Device errors: those of dsa_kv_append_rope, and DSA_DEV_ERR_VALUE.
+ */
+int dsa_kv_append_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *seqs, const dsa_new_tokens *fresh,
+                      const dsa_rope *rope, const dsa_queries *queries, const dsa_query_rows *rows,
+                      int32_t *dev_err, dsa_stream_t stream);
 
 /*
  * dsa_index_score -- block scores of every query against each visible block
@@ -287,6 +384,26 @@ int dsa_sparse_attn_prefill(const dsa_kv_cache *cache, const dsa_seqs *seqs,
                             const dsa_queries *queries, const void *q, int32_t num_q_heads,
                             const int32_t *sel, const int32_t *cnt, int32_t k_max, float sm_scale,
                             void *out, float *lse, int32_t *dev_err, dsa_stream_t stream);
+
+/*
+ * dsa_sparse_attn_decode_fp8, dsa_sparse_attn_prefill_fp8 -- the two attention
+ * calls over the 8-bit cache, with the same arguments, results, limits and
+ * workspace (dsa_sparse_attn_decode_workspace_size).  Codes, scales and queries
+ * enter the products exactly (a query entry below 2^-29 of its row's largest
+ * is rounded), softmax weights are rounded to f16, sums are fp32.  Slots that
+ * no query sees (behind its position, or never written) may hold any codes; a
+ * NaN in a code, scale or query that a row does use makes its results NaN.
+ * Device errors: those of the bf16 calls.
+ */
+int dsa_sparse_attn_decode_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *seqs, const dsa_queries *queries,
+                               const void *q, int32_t num_q_heads, const int32_t *sel, const int32_t *cnt,
+                               int32_t k_max, float sm_scale, void *out, float *lse, void *workspace,
+                               size_t workspace_bytes, int32_t *dev_err, dsa_stream_t stream);
+
+int dsa_sparse_attn_prefill_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *seqs, const dsa_queries *queries,
+                                const void *q, int32_t num_q_heads, const int32_t *sel, const int32_t *cnt,
+                                int32_t k_max, float sm_scale, void *out, float *lse, int32_t *dev_err,
+                                dsa_stream_t stream);
 
 /*
  * dsa_decode_fused -- one decode step in a single launch: dsa_kv_append, the
