@@ -137,6 +137,33 @@ void attn_schedule(AttnArgs &a, bool allow_split, bool allow_cluster = false) {
     a.interleave = (a.pair_aligned && a.num_kv_heads > 1) ? 1 : 0;
 }
 
+// Work split of the E4M3 attention kernel; returns the grid.  Whole rounds of
+// one pair per warp as long as there are pairs for every warp; the pairs left
+// over are split over the CTAs, by tiles where partial states have a workspace,
+// else by whole pairs.  A pair of few tiles is not worth a merge of eight warps:
+// its left-over round runs a pair per warp as well.
+int attn_schedule_fp8(AttnArgs &a, bool allow_split) {
+    long long C = sm_count();
+    if (C > kAttnMaxCtas) C = kAttnMaxCtas;
+    const long long pairs = (long long)a.total_q * a.num_kv_heads, W = C * kFp8Warps;
+    const long long tiles = (long long)a.k_max << a.tile_shift;
+    a.warp_rounds = (int)(pairs / W);
+    long long left = pairs - a.warp_rounds * W;
+    if (left > 0 && tiles < kFp8Warps) {
+        ++a.warp_rounds;
+        left = 0;
+    }
+    a.pair_aligned = allow_split ? 0 : 1;
+    a.total_units = left * tiles;
+    long long share = allow_split ? a.total_units : left;
+    if (share > C) share = C;
+    if (share > left * 60) share = left * 60;   // the kernel merges <= 63 partials of a pair
+    a.num_ctas = share > 0 ? (int)share : 1;
+    if (a.warp_rounds == 0) return a.num_ctas;
+    const long long full = (pairs + kFp8Warps - 1) / kFp8Warps;   // CTAs that have a pair for a warp
+    return (int)(full < C ? full : C);
+}
+
 // Cache: dsa_kv_cache or dsa_kv_cache_fp8, already checked (the caller sets the scales)
 template <typename Cache>
 int attn_args(const Cache *cache, const dsa_seqs *seqs, const dsa_queries *queries, const void *q,
@@ -716,8 +743,8 @@ int dsa_sparse_attn_decode_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *se
     char *ws = static_cast<char *>(workspace);
     a.counters = reinterpret_cast<int32_t *>(ws + L.counters);
     a.part = reinterpret_cast<float *>(ws + L.part);
-    attn_schedule(a, true, true);
-    return from_cuda(launch_sparse_attn(a, reinterpret_cast<cudaStream_t>(stream)));
+    const int ctas = attn_schedule_fp8(a, true);
+    return from_cuda(launch_sparse_attn_fp8(a, ctas, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int dsa_sparse_attn_prefill_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *seqs, const dsa_queries *queries,
@@ -728,8 +755,8 @@ int dsa_sparse_attn_prefill_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *s
     int rc = attn_common_fp8(cache, seqs, queries, q, num_q_heads, sel, cnt, k_max, sm_scale, out, lse, dev_err, a);
     if (rc) return rc;
     if (queries->total_q == 0) return DSA_OK;
-    attn_schedule(a, false);   // whole pairs per CTA: no partial states, no workspace
-    return from_cuda(launch_sparse_attn(a, reinterpret_cast<cudaStream_t>(stream)));
+    const int ctas = attn_schedule_fp8(a, false);   // whole pairs: no partial states, no workspace
+    return from_cuda(launch_sparse_attn_fp8(a, ctas, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

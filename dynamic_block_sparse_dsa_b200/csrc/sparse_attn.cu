@@ -45,14 +45,15 @@
 
 #include "dsa_kernels.h"
 #include "dsa_tma.cuh"
-#include "attn_fp8.cuh"
 #include "decode_fused.cuh"
 
 namespace dsa {
 
 namespace {
+constexpr int kConsumerWarps = 4;
+constexpr int kAttnThreads = (kConsumerWarps + 1) * 32;
 constexpr int kHalf = kBlockSize * 128;            // 8 KiB: 64 rows x 128 B (one swizzled half)
-constexpr int kV8 = fp8::kTileBytes;               // E4M3: the V tile behind the K tile of a stage
+constexpr int kStageBytes = 4 * kHalf;             // K lo, K hi, V lo, V hi
 constexpr int kQHalf = 16 * 128;                   // 16 query rows x 128 B
 constexpr int kQSlotBytes = 2 * kQHalf;
 constexpr int kSegSlots = 2;                       // query tile + pair facts, double buffered
@@ -61,16 +62,14 @@ constexpr int kMaxSmemSeqs = 256;                  // cu_q entries cached in sha
 // int words after the barriers
 constexpr int kWAbort = 0, kWLast = 1, kWNever = 2, kWTag = 3;
 constexpr int kWFill = 4;                           // [kMaxStages] item index the stage was last armed for
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 8;
 constexpr int kWItemBlk = kWFill + kMaxStages;      // [kMaxStages] logical block of that item
 constexpr int kWItemSeg = kWItemBlk + kMaxStages;   // [kMaxStages] segment of that item
 constexpr int kWSegEndCnt = kWItemSeg + kMaxStages; // [kSegSlots] items issued when the segment ended
 constexpr int kWSegEndTag = kWSegEndCnt + kSegSlots;  // [kSegSlots] which segment that count belongs to
 constexpr int kWSegInfo = kWSegEndTag + kSegSlots;  // [kSegSlots][4]: t, kvh, p, n_vis
 constexpr int kWSelLast = kWSegInfo + 4 * kSegSlots;   // fused select: this CTA merges
-constexpr int kWScaleK = kWSelLast + 1;             // [kMaxStages] E4M3: the item's K scale (float bits)
-constexpr int kWScaleV = kWScaleK + kMaxStages;     // [kMaxStages] and its V scale
-constexpr int kNumWords = kWScaleV + kMaxStages;
+constexpr int kNumWords = kWSelLast + 1;
 constexpr float kLn2 = 0.6931471805599453f;
 // most CTAs whose ranges can cover one pair (the host caps the split at 60)
 constexpr int kMaxSplitSlots = 63;
@@ -78,20 +77,15 @@ constexpr int kMaxSplitSlots = 63;
 constexpr uint32_t kInboxRowBytes = 128 * 4 + 2 * 4;
 
 // shared-memory plan for NT head tiles: a group of <= 8 heads leaves room for
-// more ring stages; 16-head groups need the larger merge buffer.  An E4M3
-// stage is half as large (K tile, V tile: 8 KiB each) and takes a warp longer
-// per byte (the conversions), so it runs with twice the stages and consumers.
-template <int NT, bool kFp8>
+// a sixth ring stage; 16-head groups need the larger merge buffer
+template <int NT>
 struct Plan {
-    static constexpr int kWarps = kFp8 ? 8 : 4;        // consumer warps
-    static constexpr int kThreads = (kWarps + 1) * 32;
-    static constexpr int kStageBytes = kFp8 ? 2 * fp8::kTileBytes : 4 * kHalf;   // bf16: K lo, K hi, V lo, V hi
-    static constexpr int kStages = kFp8 ? (NT == 1 ? 10 : 8) : (NT == 1 ? 6 : 5);
+    static constexpr int kStages = NT == 1 ? 6 : 5;
     static constexpr int kMergeRows = 8 * NT;
     static constexpr int kOffQ = kStages * kStageBytes;
     static constexpr int kOffMergeO = kOffQ + kSegSlots * kQSlotBytes;
-    static constexpr int kOffMergeML = kOffMergeO + kWarps * kMergeRows * kMergeStride * 4;
-    static constexpr int kOffCuq = kOffMergeML + kWarps * 16 * 2 * 4;
+    static constexpr int kOffMergeML = kOffMergeO + kConsumerWarps * kMergeRows * kMergeStride * 4;
+    static constexpr int kOffCuq = kOffMergeML + kConsumerWarps * 16 * 2 * 4;
     static constexpr int kOffRb = (kOffCuq + (kMaxSmemSeqs + 1) * 4 + 4 + 7) / 8 * 8;
     static constexpr int kOffBars = kOffRb + (kAttnMaxCtas + 1) * 8;
     static constexpr int kNumBars = 2 * kStages + 2 * kSegSlots + 1;   // + the cluster inbox
@@ -100,15 +94,15 @@ struct Plan {
     static constexpr int kOffInbox = (kOffWords + kNumWords * 4 + 15) / 16 * 16;
     static constexpr int kSmemBytes = kOffInbox + kMergeRows * kAttnPartStride * 4 + 1024;   // + base alignment slack
     static_assert(kStages <= kMaxStages, "stage words");
-    static_assert(kFp8 || fused::kScratchBytes <= kStages * kStageBytes, "fused select scratch fits the ring");
+    static_assert(fused::kScratchBytes <= kStages * kStageBytes, "fused select scratch fits the ring");
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
-template <int NT, bool kFp8>
+template <int NT>
 struct Smem {
-    using P = Plan<NT, kFp8>;
+    using P = Plan<NT>;
     uint32_t base;   // 1 KiB aligned shared address
-    __device__ uint32_t stage(int s) const { return base + s * P::kStageBytes; }
+    __device__ uint32_t stage(int s) const { return base + s * kStageBytes; }
     __device__ uint32_t qslot(int s) const { return base + P::kOffQ + s * kQSlotBytes; }
     __device__ uint32_t full(int s) const { return base + P::kOffBars + 8 * s; }
     __device__ uint32_t empty(int s) const { return base + P::kOffBars + 8 * (P::kStages + s); }
@@ -133,13 +127,6 @@ __device__ __forceinline__ unit_t range_begin(const AttnArgs &a, int c) {
     return (unit_t)((unsigned long long)c * (unsigned long long)a.total_units / (unsigned)a.num_ctas);
 }
 
-// natural log-sum-exp from a base-2 maximum and sum; -inf for an empty row.
-// (A NaN sum is kept over the E4M3 cache and reads as empty over the bf16 one.)
-template <bool kFp8>
-__device__ __forceinline__ float lse_of(float m, float l) {
-    return (kFp8 ? !(l <= 0.f) : l > 0.f) ? (m + log2f(l)) * kLn2 : -INFINITY;
-}
-
 // sequence of query t: last s with cu_q[s] <= t, from the shared-memory copy when it fits
 __device__ __forceinline__ int seq_of(const AttnArgs &a, const int *s_cuq, int t) {
     if (a.num_seqs + 1 > kMaxSmemSeqs) return find_seq(a.cu_q, a.num_seqs, t);
@@ -156,18 +143,15 @@ __device__ __forceinline__ int seq_of(const AttnArgs &a, const int *s_cuq, int t
 // single-launch decode step -- the select and append phases of
 // decode_fused.cuh run first, and the producer waits for each query's
 // selection before reading it.
-// kFp8: the pools hold E4M3 codes with one scale per 64-token tile and KV head.
-template <int NT, bool kFused, bool kFp8>
-__global__ void __launch_bounds__(Plan<NT, kFp8>::kThreads, 1)
+template <int NT, bool kFused>
+__global__ void __launch_bounds__(kAttnThreads, 1)
 sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ CUtensorMap tm_q, AttnArgs a, FusedArgs f) {
-    static_assert(!(kFused && kFp8), "the single-launch step works on the bf16 cache");
-    using P = Plan<NT, kFp8>;
-    constexpr int kStages = P::kStages, kStageBytes = P::kStageBytes;
-    constexpr int kConsumerWarps = P::kWarps, kAttnThreads = P::kThreads;
+    using P = Plan<NT>;
+    constexpr int kStages = P::kStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
-    Smem<NT, kFp8> sm{(raw + 1023u) & ~1023u};
+    Smem<NT> sm{(raw + 1023u) & ~1023u};
     uint8_t *gbase = smem_raw + (sm.base - raw);   // generic pointer of the aligned base
     volatile int *W = reinterpret_cast<volatile int *>(gbase + P::kOffWords);
     volatile int *s_abort = W + kWAbort;
@@ -279,7 +263,6 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             // sequence (blk) and the tile's first pool row (page); n_vis counts
             // the query's visible 64-token tiles
             int t = 0, kvh = 0, s = 0, p = 0, n_vis = 0, blk = -1, page = -1;
-            float scale_k = 0.f, scale_v = 0.f;
             if (in) {
                 const unit_t pair = uu / K;
                 const int ju = (int)(uu - pair * K);
@@ -311,11 +294,6 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         if (pg < 0 || pg >= a.num_pages) err_bits |= DSA_DEV_ERR_PAGE;
                         else if (tile < n_vis) { blk = tile; page = (pg << a.block_shift) + (sub << 6); }
                         // tiles past the query's position (own block only) hold no visible token
-                        if (kFp8 && page >= 0) {   // written by an append before this launch, as the codes are
-                            const size_t i = (size_t)(page >> 6) * Hkv + kvh;
-                            scale_k = ld_ordered_cg(a.k_scale + i);
-                            scale_v = ld_ordered_cg(a.v_scale + i);
-                        }
                     }
                 }
             }
@@ -360,8 +338,6 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     todo &= todo - 1;
                     const int ib = __shfl_sync(0xffffffffu, blk, src);
                     const int ipg = __shfl_sync(0xffffffffu, page, src);
-                    const float isk = kFp8 ? __shfl_sync(0xffffffffu, scale_k, src) : 0.f;
-                    const float isv = kFp8 ? __shfl_sync(0xffffffffu, scale_v, src) : 0.f;
                     if (lane == 0 && !*s_abort) {
                         const int st = item % kStages;
                         if (item >= kStages && !mbar_wait(sm.empty(st), ((item / kStages) - 1) & 1, s_abort)) {
@@ -369,24 +345,15 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         } else {
                             W[kWItemBlk + st] = ib;
                             W[kWItemSeg + st] = seg;
-                            if (kFp8) {
-                                W[kWScaleK + st] = __float_as_int(isk);
-                                W[kWScaleV + st] = __float_as_int(isv);
-                            }
                             __threadfence_block();
                             W[kWFill + st] = item;
                             const uint32_t dst = sm.stage(st);
                             mbar_arrive_expect_tx(sm.full(st), kStageBytes);
                             const int z = ipg;   // the tile's first row in the pool
-                            if constexpr (kFp8) {
-                                tma_load_3d(dst, &tm_k, 0, pkvh, z, sm.full(st));
-                                tma_load_3d(dst + kV8, &tm_v, 0, pkvh, z, sm.full(st));
-                            } else {
-                                tma_load_3d(dst, &tm_k, 0, pkvh, z, sm.full(st));
-                                tma_load_3d(dst + kHalf, &tm_k, 64, pkvh, z, sm.full(st));
-                                tma_load_3d(dst + 2 * kHalf, &tm_v, 0, pkvh, z, sm.full(st));
-                                tma_load_3d(dst + 3 * kHalf, &tm_v, 64, pkvh, z, sm.full(st));
-                            }
+                            tma_load_3d(dst, &tm_k, 0, pkvh, z, sm.full(st));
+                            tma_load_3d(dst + kHalf, &tm_k, 64, pkvh, z, sm.full(st));
+                            tma_load_3d(dst + 2 * kHalf, &tm_v, 0, pkvh, z, sm.full(st));
+                            tma_load_3d(dst + 3 * kHalf, &tm_v, 64, pkvh, z, sm.full(st));
                         }
                     }
                     ++item;
@@ -444,9 +411,6 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 
         // Q^T fragments (B operand of S^T = K Q^T): k = dims, n = query heads
         uint32_t qb[8][NT][2];
-        float qmul[NT][2];   // E4M3: accumulator -> base-2 logits, per head
-        if constexpr (kFp8) fp8::load_queries<NT>(sm.qslot(qs), kQHalf, ok, a.scale_log2, qb, qmul);
-        else
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -460,7 +424,6 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
             }
         // O^T accumulators: dims 16*dm + g (+8) x heads 8*nt + 2*cq (+1)
-        // (E4M3: dims 16*dm + 2*g (+1))
         float o[8][NT][4];
         float m_run[NT][2], l_run[NT][2];
 #pragma unroll
@@ -498,7 +461,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             }
             __syncwarp();
             const int blk = W[kWItemBlk + st];
-            const uint32_t tk = sm.stage(st), tv = tk + (kFp8 ? kV8 : 2 * kHalf);
+            const uint32_t tk = sm.stage(st), tv = tk + 2 * kHalf;
             // the last visible token of this tile (only the query's own tile is partial)
             const int lim = (blk == pnv - 1) ? pp - blk * kBlockSize : kBlockSize - 1;
             if (lim < kBlockSize - 1) {
@@ -506,21 +469,12 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 // there (nothing appended yet); a zero softmax weight times a NaN
                 // or infinite value is still NaN, so their value rows are cleared
                 // (both 128-byte halves, 16-byte chunks at their swizzled place)
-                if constexpr (kFp8) {
-                    for (int e = lane; e < (kBlockSize - 1 - lim) * 8; e += 32)
-                        st_shared_zero16(tv + swz128(lim + 1 + (e >> 3), e & 7));
-                } else {
-                    for (int e = lane; e < (kBlockSize - 1 - lim) * 16; e += 32) {
-                        const int r = lim + 1 + (e >> 4), cc = e & 15;
-                        st_shared_zero16(tv + (cc >> 3) * kHalf + swz128(r, cc & 7));
-                    }
+                for (int e = lane; e < (kBlockSize - 1 - lim) * 16; e += 32) {
+                    const int r = lim + 1 + (e >> 4), cc = e & 15;
+                    st_shared_zero16(tv + (cc >> 3) * kHalf + swz128(r, cc & 7));
                 }
                 __syncwarp();
             }
-            if constexpr (kFp8) {
-                fp8::attend_tile<NT>(tk, tv, lim, __int_as_float(W[kWScaleK + st]), __int_as_float(W[kWScaleV + st]),
-                                     qb, qmul, o, m_run, l_run);
-            } else {
             // ---- S^T = K Q^T: 4 m-tiles of 16 tokens x NT n-tiles of 8 heads
             float sc[4][NT][4];
 #pragma unroll
@@ -600,7 +554,6 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(o[dm][nt], va, pb[nt][0], pb[nt][1]);
                 }
             }
-            }
             // generic-proxy stores (the cleared rows) before the TMA refills the stage
             if (lim < kBlockSize - 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -633,17 +586,11 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             float *row1 = row0 + kMergeStride;
 #pragma unroll
             for (int dm = 0; dm < 8; ++dm) {
-                if constexpr (kFp8) {
-                    const int d = 16 * dm + 2 * g;
-                    *reinterpret_cast<float2 *>(row0 + d) = make_float2(o[dm][nt][0], o[dm][nt][2]);
-                    *reinterpret_cast<float2 *>(row1 + d) = make_float2(o[dm][nt][1], o[dm][nt][3]);
-                } else {
-                    const int d = 16 * dm + g;
-                    row0[d] = o[dm][nt][0];
-                    row1[d] = o[dm][nt][1];
-                    row0[d + 8] = o[dm][nt][2];
-                    row1[d + 8] = o[dm][nt][3];
-                }
+                const int d = 16 * dm + g;
+                row0[d] = o[dm][nt][0];
+                row1[d] = o[dm][nt][1];
+                row0[d + 8] = o[dm][nt][2];
+                row1[d + 8] = o[dm][nt][3];
             }
             if (g == 0) {
                 s_ml[(warp * 16 + h0) * 2] = m_run[nt][0];
@@ -664,7 +611,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             // the two halves of the pair meet in rank 0's shared memory: rank 1
             // stores its merged state there and arrives on rank 0's inbox
             // barrier; rank 0 combines it with its own and writes the output
-            constexpr int kRowsPT = 8 * NT / kConsumerWarps;
+            constexpr int kRowsPT = 2 * NT;
             float Mo[kRowsPT], Lo[kRowsPT], Ao[kRowsPT][4];
 #pragma unroll
             for (int i = 0; i < kRowsPT; ++i) {
@@ -735,7 +682,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     const float inv = L > 0.f ? 1.f / L : 0.f;
                     *reinterpret_cast<uint2 *>(a.out + (out_row + r) * kHeadDim + d0) =
                         make_uint2(pack_bf16x2(o0 * inv, o1 * inv), pack_bf16x2(o2 * inv, o3 * inv));
-                    if (a.lse && d0 == 0) a.lse[out_row + r] = lse_of<kFp8>(Mn, L);
+                    if (a.lse && d0 == 0) a.lse[out_row + r] = L > 0.f ? (Mn + log2f(L)) * kLn2 : -INFINITY;
                 }
             }
             __syncwarp();
@@ -765,7 +712,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const float inv = L > 0.f ? 1.f / L : 0.f;
                 *reinterpret_cast<uint2 *>(a.out + (out_row + r) * kHeadDim + d0) =
                     make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-                if (a.lse && d0 == 0) a.lse[out_row + r] = lse_of<kFp8>(M, L);
+                if (a.lse && d0 == 0) a.lse[out_row + r] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
             } else {
                 float *dst = a.part + ((size_t)slot * G + r) * kAttnPartStride;
                 *reinterpret_cast<float4 *>(dst + d0) = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -797,7 +744,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 // each thread owns kRowsPT (row, 4-column) pieces; the loads of
                 // all of them and of a batch of slots are issued before any is
                 // used, so the merge costs one L2 round trip per batch
-                constexpr int kRowsPT = 8 * NT / kConsumerWarps;   // 8 * NT rows * 32 pieces / consumer threads
+                constexpr int kRowsPT = 2 * NT;                 // 8 * NT rows * 32 pieces / 128 threads
                 constexpr int kBatch = NT == 1 ? 4 : 2;         // slots per round trip
                 float M[kRowsPT], L[kRowsPT], acc[kRowsPT][4];
 #pragma unroll
@@ -856,7 +803,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     *reinterpret_cast<uint2 *>(a.out + (out_row + r) * kHeadDim + d0) =
                         make_uint2(pack_bf16x2(acc[i][0] * inv, acc[i][1] * inv),
                                    pack_bf16x2(acc[i][2] * inv, acc[i][3] * inv));
-                    if (a.lse && d0 == 0) a.lse[out_row + r] = lse_of<kFp8>(M[i], L[i]);
+                    if (a.lse && d0 == 0) a.lse[out_row + r] = L[i] > 0.f ? (M[i] + log2f(L[i])) * kLn2 : -INFINITY;
                 }
                 if (tid == 0) a.counters[pair] = 0;
             }
@@ -917,11 +864,10 @@ struct MapKey {
     int dev;
     const void *k, *v, *q;
     int num_pages, num_kv_heads, block_shift, total_q, num_q_heads;
-    bool fp8;
     bool operator==(const MapKey &o) const {
         return dev == o.dev && k == o.k && v == o.v && q == o.q && num_pages == o.num_pages &&
                num_kv_heads == o.num_kv_heads && block_shift == o.block_shift && total_q == o.total_q &&
-               num_q_heads == o.num_q_heads && fp8 == o.fp8;
+               num_q_heads == o.num_q_heads;
     }
 };
 constexpr int kMapCache = 16;
@@ -934,7 +880,7 @@ cudaError_t make_maps(const AttnArgs &a, AttnMaps &m) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
     const MapKey key{dev, a.k_pool, a.v_pool, a.q, a.num_pages, a.num_kv_heads, a.block_shift, a.total_q,
-                     a.num_q_heads, a.k_scale != nullptr};
+                     a.num_q_heads};
     {
         std::lock_guard<std::mutex> lock(g_map_mu);
         for (int i = 0; i < g_map_n; ++i)
@@ -956,23 +902,19 @@ cudaError_t make_maps(const AttnArgs &a, AttnMaps &m) {
 cudaError_t encode_maps(const AttnArgs &a, AttnMaps &m) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorNotSupported;
-    // K / V pool: dims (head_dim, kv_head, page*B+token), boxes of 128 bytes (64
-    // dims of bf16, all 128 of E4M3) x 1 head x 64 tokens (one tile)
-    const bool fp8 = a.k_scale != nullptr;
-    const cuuint64_t el = fp8 ? 1 : 2;
-    const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    // K / V pool: dims (head_dim, kv_head, page*B+token), boxes of 64 dims x 1 head x 64 tokens (one tile)
     const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)a.num_kv_heads,
                                 (cuuint64_t)a.num_pages << a.block_shift};
-    const cuuint64_t strides[2] = {kHeadDim * el, (cuuint64_t)a.num_kv_heads * kHeadDim * el};
-    const cuuint32_t box[3] = {(cuuint32_t)(128 / el), 1, kBlockSize};
+    const cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)a.num_kv_heads * kHeadDim * 2};
+    const cuuint32_t box[3] = {64, 1, kBlockSize};
     const cuuint32_t estr[3] = {1, 1, 1};
-    if (enc(&m.k, type, 3, const_cast<void *>(a.k_pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
-        CUDA_SUCCESS)
+    if (enc(&m.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.k_pool), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    if (enc(&m.v, type, 3, const_cast<void *>(a.v_pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
-        CUDA_SUCCESS)
+    if (enc(&m.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.v_pool), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     // Q: rows (query, head), boxes of 64 dims x 16 rows; rows past the end read as zero
     const cuuint64_t qdims[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)a.total_q * a.num_q_heads};
@@ -985,12 +927,6 @@ cudaError_t encode_maps(const AttnArgs &a, AttnMaps &m) {
     return cudaSuccess;
 }
 
-template <int NT, bool kFused, bool kFp8>
-cudaError_t set_smem_attr() {
-    return cudaFuncSetAttribute(sparse_attn_kernel<NT, kFused, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Plan<NT, kFp8>::kSmemBytes);
-}
-
 // the shared-memory opt-in of every instantiation, once per device
 cudaError_t set_smem_attrs() {
     static unsigned long long attr_done = 0;
@@ -998,58 +934,20 @@ cudaError_t set_smem_attrs() {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && (attr_done & (1ull << dev))) return cudaSuccess;
-    e = set_smem_attr<1, false, false>();
-    if (e == cudaSuccess) e = set_smem_attr<2, false, false>();
-    if (e == cudaSuccess) e = set_smem_attr<1, true, false>();
-    if (e == cudaSuccess) e = set_smem_attr<2, true, false>();
-    if (e == cudaSuccess) e = set_smem_attr<1, false, true>();
-    if (e == cudaSuccess) e = set_smem_attr<2, false, true>();
+    e = cudaFuncSetAttribute(sparse_attn_kernel<1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Plan<1>::kSmemBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(sparse_attn_kernel<2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Plan<2>::kSmemBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(sparse_attn_kernel<1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Plan<1>::kSmemBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(sparse_attn_kernel<2, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Plan<2>::kSmemBytes);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done |= 1ull << dev;
     return cudaSuccess;
-}
-
-template <int NT, bool kFp8>
-cudaError_t launch_attn(const AttnArgs &a, const AttnMaps &m, cudaStream_t stream) {
-    using P = Plan<NT, kFp8>;
-    const FusedArgs none{};
-    if (!a.cluster2)
-        return launch_pdl(sparse_attn_kernel<NT, false, kFp8>, dim3(a.num_ctas), dim3(P::kThreads), P::kSmemBytes,
-                          stream, m.k, m.v, m.q, a, none);
-    // pairs of CTAs on one GPC, merging through distributed shared memory
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.num_ctas);
-    cfg.blockDim = dim3(P::kThreads);
-    cfg.dynamicSmemBytes = P::kSmemBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sparse_attn_kernel<NT, false, kFp8>, m.k, m.v, m.q, a, none);
-}
-
-template <int NT>
-cudaError_t launch_fused(const AttnArgs &a, const FusedArgs &f, const AttnMaps &m, cudaStream_t stream) {
-    // every CTA resident at once: the attention phase waits on selections
-    // that other CTAs publish
-    using P = Plan<NT, false>;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.num_ctas);
-    cfg.blockDim = dim3(P::kThreads);
-    cfg.dynamicSmemBytes = P::kSmemBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sparse_attn_kernel<NT, true, false>, m.k, m.v, m.q, a, f);
 }
 }  // namespace
 
@@ -1059,8 +957,33 @@ cudaError_t launch_sparse_attn(const AttnArgs &a, cudaStream_t stream) {
     cudaError_t e = make_maps(a, m);
     if (e == cudaSuccess) e = set_smem_attrs();
     if (e != cudaSuccess) return e;
-    if (a.k_scale) return a.group <= 8 ? launch_attn<1, true>(a, m, stream) : launch_attn<2, true>(a, m, stream);
-    return a.group <= 8 ? launch_attn<1, false>(a, m, stream) : launch_attn<2, false>(a, m, stream);
+    const FusedArgs none{};
+    if (a.cluster2) {   // pairs of CTAs on one GPC, merging through distributed shared memory
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(a.num_ctas);
+        cfg.blockDim = dim3(kAttnThreads);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 2;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        if (a.group <= 8) {
+            cfg.dynamicSmemBytes = Plan<1>::kSmemBytes;
+            return cudaLaunchKernelEx(&cfg, sparse_attn_kernel<1, false>, m.k, m.v, m.q, a, none);
+        }
+        cfg.dynamicSmemBytes = Plan<2>::kSmemBytes;
+        return cudaLaunchKernelEx(&cfg, sparse_attn_kernel<2, false>, m.k, m.v, m.q, a, none);
+    }
+    if (a.group <= 8)
+        return launch_pdl(sparse_attn_kernel<1, false>, dim3(a.num_ctas), dim3(kAttnThreads), Plan<1>::kSmemBytes,
+                          stream, m.k, m.v, m.q, a, none);
+    return launch_pdl(sparse_attn_kernel<2, false>, dim3(a.num_ctas), dim3(kAttnThreads), Plan<2>::kSmemBytes,
+                      stream, m.k, m.v, m.q, a, none);
 }
 
 cudaError_t launch_decode_fused(const AttnArgs &a, const FusedArgs &f, cudaStream_t stream) {
@@ -1069,7 +992,23 @@ cudaError_t launch_decode_fused(const AttnArgs &a, const FusedArgs &f, cudaStrea
     cudaError_t e = make_maps(a, m);
     if (e == cudaSuccess) e = set_smem_attrs();
     if (e != cudaSuccess) return e;
-    return a.group <= 8 ? launch_fused<1>(a, f, m, stream) : launch_fused<2>(a, f, m, stream);
+    // every CTA resident at once: the attention phase waits on selections
+    // that other CTAs publish
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.num_ctas);
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (a.group <= 8) {
+        cfg.dynamicSmemBytes = Plan<1>::kSmemBytes;
+        return cudaLaunchKernelEx(&cfg, sparse_attn_kernel<1, true>, m.k, m.v, m.q, a, f);
+    }
+    cfg.dynamicSmemBytes = Plan<2>::kSmemBytes;
+    return cudaLaunchKernelEx(&cfg, sparse_attn_kernel<2, true>, m.k, m.v, m.q, a, f);
 }
 
 }  // namespace dsa

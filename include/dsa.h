@@ -389,7 +389,7 @@ int dsa_sparse_attn_prefill(const dsa_kv_cache *cache, const dsa_seqs *seqs,
  * dsa_sparse_attn_decode_fp8, dsa_sparse_attn_prefill_fp8 -- the two attention
  * calls over the 8-bit cache, with the same arguments, results, limits and
  * workspace (dsa_sparse_attn_decode_workspace_size).  Codes, scales and queries
- * enter the products exactly (a query entry below 2^-29 of its row's largest
+ * enter the products exactly (a query entry below 2^-31 of its row's largest
  * is rounded), softmax weights are rounded to f16, sums are fp32.  Slots that
  * no query sees (behind its position, or never written) may hold any codes; a
  * NaN in a code, scale or query that a row does use makes its results NaN.

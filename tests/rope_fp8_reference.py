@@ -9,6 +9,9 @@ Roundings (half a step: bf16 2^-8, f16 2^-11, fp32 2^-24, E4M3 2^-4 relative):
   * a logit is a dot product of 128 exact products summed in fp32 (in any
     order: at most 128 * 2^-24 of the sum of their magnitudes) with a few fp32
     factors, 140 * 2^-24 in all; 2^x is within 2^-22;
+  * over the 8-bit cache a query entry is taken in f16, scaled by the power of
+    two that brings the row's largest entry to [2^14, 2^15): bf16's 8 bits fit,
+    and where f16 is subnormal it is off by at most 2^-25, 2^-39 of the largest;
   * a softmax weight rounds to f16 (2^-11 relative; 2^-25 of the largest weight
     below the type's normal range) over the 8-bit cache, to bf16 (2^-8) over
     the bf16 one; the weighted sum accumulates in fp32 over n tokens, and the
@@ -115,6 +118,7 @@ def attention(q, k_pool, v_pool, table, block, q_seq, q_pos, sel, cnt, sm_scale,
             out[t, h] = (w / norm) @ vh
             lse[t, h] = top + norm.log()
             delta = float((kh.abs() @ qh.abs()).max()) * sm_scale * 140 * 2.0 ** -24 + 2.0 ** -21
+            delta += float(kh.abs().sum(1).max() * qh.abs().max()) * sm_scale * 2.0 ** -39
             mass = (w / norm) @ vh.abs()
             tiny = 2.0 ** -25 / norm * vh.abs().sum(0)
             otol[t, h] = out[t, h].abs() * 2.0 ** -8 + mass * (2 * delta + p_half + n * 2.0 ** -24) + tiny + 1e-30
