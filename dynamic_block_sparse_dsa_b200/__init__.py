@@ -31,6 +31,7 @@ Layout", "Differentiated Adaptation of Prefill and Decode".
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from dataclasses import dataclass
@@ -81,6 +82,43 @@ def _expect(t: torch.Tensor, dtype, name):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _at(t: torch.Tensor, dtype, dev: int, name: str) -> int:
+    """Address of a contiguous ``dtype`` tensor on device ``dev``."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    at = t.get_device()
+    if at != dev:
+        _wrong_device(at, dev, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _wrong_device(at: int, dev: int, name: str):
+    if at < 0:
+        raise ValueError("dynamic_block_sparse_dsa_b200 works on CUDA tensors only (no CPU path)")
+    raise ValueError(f"{name} is on cuda:{at}, the call's other tensors on cuda:{dev}")
+
+
+def _current(t: torch.Tensor) -> int:
+    """The device of ``t``, which has to be the current one: the library launches there."""
+    dev = t.get_device()
+    if dev < 0:
+        _wrong_device(dev, dev, "")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _on(stream):
+    """Allocations of a call on ``stream`` belong to that stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 @dataclass
 class PagedKVCache:
     """Block-paged pools: k/v bf16 [num_pages][block_size][num_kv_heads][128], kc int8
@@ -99,6 +137,18 @@ class PagedKVCache:
                              self.kc_pool.shape[1])
 
     index_ctype = ctype
+
+    def packed(self, dev: int) -> bytes:
+        """The C description (dsa_kv_cache) of tensors on device ``dev``."""
+        kp, vp, kc = self.k_pool, self.v_pool, self.kc_pool
+        n, bs, hkv, d = kp.shape
+        if vp.shape != kp.shape:
+            raise ValueError("k_pool and v_pool differ in shape")
+        pages, idx_dim = kc.shape
+        if kc.element_size() != 1 or pages != n:
+            raise ValueError("kc_pool must hold one byte per element and one row per page")
+        return _lib.pack_cache(_at(kp, torch.bfloat16, dev, "k_pool"), _at(vp, torch.bfloat16, dev, "v_pool"),
+                               _at(kc, kc.dtype, dev, "kc_pool"), n, bs, hkv, d, idx_dim)
 
     @property
     def num_kv_heads(self) -> int:
@@ -122,28 +172,29 @@ class PagedKVCacheFP8:
     k_scale: torch.Tensor
     v_scale: torch.Tensor
 
-    def ctype(self) -> _lib.KvCacheFp8C:
-        kp, vp = self.k_pool, self.v_pool
+    def packed(self, dev: int) -> bytes:
+        """The C description (dsa_kv_cache_fp8) of tensors on device ``dev``."""
+        kp, vp, kc = self.k_pool, self.v_pool, self.kc_pool
         if kp.dtype not in _CODES or vp.dtype not in _CODES:
             raise ValueError(f"k_pool and v_pool must hold E4M3 codes, got {kp.dtype} and {vp.dtype}")
         n, bs, hkv, d = kp.shape
         if vp.shape != kp.shape:
             raise ValueError("k_pool and v_pool differ in shape")
-        if self.kc_pool.element_size() != 1 or self.kc_pool.shape[0] != n:
+        pages, idx_dim = kc.shape
+        if kc.element_size() != 1 or pages != n:
             raise ValueError("kc_pool must hold one byte per element and one row per page")
-        _expect(self.k_scale, torch.float32, "k_scale")
-        _expect(self.v_scale, torch.float32, "v_scale")
         tiles = (n, bs // TILE, hkv)
         if self.k_scale.shape != tiles or self.v_scale.shape != tiles:
             raise ValueError(f"k_scale and v_scale must be {list(tiles)}")
-        return _lib.KvCacheFp8C(_addr(kp), _addr(vp), _addr(self.kc_pool), _addr(self.k_scale), _addr(self.v_scale),
-                                n, bs, hkv, d, self.kc_pool.shape[1])
+        return _lib.pack_cache_fp8(_at(kp, kp.dtype, dev, "k_pool"), _at(vp, vp.dtype, dev, "v_pool"),
+                                   _at(kc, kc.dtype, dev, "kc_pool"), _at(self.k_scale, torch.float32, dev, "k_scale"),
+                                   _at(self.v_scale, torch.float32, dev, "v_scale"), n, bs, hkv, d, idx_dim)
 
     def index_ctype(self) -> _lib.KvCacheC:
         """What the indexer and selection calls read: the coarse keys and the sizes."""
-        c = self.ctype()
-        return _lib.KvCacheC(c.k_pool, c.v_pool, c.kc_pool, c.num_pages, c.block_size, c.num_kv_heads, c.head_dim,
-                             c.idx_dim)
+        n, bs, hkv, d = self.k_pool.shape
+        return _lib.KvCacheC(_addr(self.k_pool), _addr(self.v_pool), _addr(self.kc_pool), n, bs, hkv, d,
+                             self.kc_pool.shape[1])
 
     @property
     def num_kv_heads(self) -> int:
@@ -169,15 +220,15 @@ class Rotary:
     pair_axis: Optional[torch.Tensor] = None
     scale: float = 1.0
 
-    def ctype(self) -> _lib.RopeC:
-        _expect(self.inv_freq, torch.float32, "inv_freq")
-        half = self.inv_freq.numel()
+    def packed(self, dev: int) -> bytes:
+        """The C description (dsa_rope) of tensors on device ``dev``."""
+        half, axis = self.inv_freq.numel(), None
         if self.num_axes > 1:
             if self.pair_axis is None or self.pair_axis.numel() != half:
                 raise ValueError("num_axes > 1 needs pair_axis, one entry per pair")
-            _expect(self.pair_axis, torch.int32, "pair_axis")
-        return _lib.RopeC(_addr(self.inv_freq), _addr(self.pair_axis) if self.num_axes > 1 else None, 2 * half,
-                          1 if self.interleaved else 0, self.num_axes, self.scale)
+            axis = _at(self.pair_axis, torch.int32, dev, "pair_axis")
+        return _lib.pack_rope(_at(self.inv_freq, torch.float32, dev, "inv_freq"), axis or 0, 2 * half,
+                              1 if self.interleaved else 0, self.num_axes, self.scale)
 
 
 @dataclass
@@ -192,6 +243,14 @@ class SeqBatch:
         ns, mb = self.block_table.shape
         return _lib.SeqsC(_addr(self.block_table), mb, _addr(self.seq_lens), ns)
 
+    def packed(self, dev: int) -> bytes:
+        """The C description (dsa_seqs) of tensors on device ``dev``."""
+        ns, mb = self.block_table.shape
+        if self.seq_lens.numel() != ns:
+            raise ValueError(f"seq_lens must have an entry for each of the {ns} sequences")
+        return _lib.pack_seqs(_at(self.block_table, torch.int32, dev, "block_table"), mb,
+                              _at(self.seq_lens, torch.int32, dev, "seq_lens"), ns)
+
 
 @dataclass
 class QueryBatch:
@@ -203,6 +262,11 @@ class QueryBatch:
         _expect(self.cu_q, torch.int32, "cu_q")
         _expect(self.q_pos, torch.int32, "q_pos")
         return _lib.QueriesC(_addr(self.cu_q), _addr(self.q_pos), self.q_pos.numel())
+
+    def packed(self, dev: int) -> bytes:
+        """The C description (dsa_queries) of tensors on device ``dev``."""
+        return _lib.pack_queries(_at(self.cu_q, torch.int32, dev, "cu_q"), _at(self.q_pos, torch.int32, dev, "q_pos"),
+                                 self.q_pos.numel())
 
     @property
     def total_q(self) -> int:
@@ -219,81 +283,78 @@ def kv_append(cache: PagedKVCache, seqs: SeqBatch, cu_new: torch.Tensor, k_new: 
         _ptr(kc_new), _ptr(dev_err), _stream(stream)))
 
 
-def _rows(t: torch.Tensor, heads: Optional[int], name: str):
-    """(address, elements from one token to the next) of bf16 [tokens][heads][128] rows;
-    only the tokens may be apart (slices of a packed projection)."""
-    _expect(t, torch.bfloat16, name)
-    if t.dim() != 3 or t.shape[2] != HEAD_DIM or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [tokens][{'heads' if heads is None else heads}][{HEAD_DIM}], got "
-                         f"{list(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError("dynamic_block_sparse_dsa_b200 works on CUDA tensors only (no CPU path)")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != HEAD_DIM):
-        raise ValueError(f"the heads of each token of {name} must be contiguous")
+def _rows(t: torch.Tensor, dev: int, name: str):
+    """(address, tokens, heads, elements from one token to the next) of bf16
+    [tokens][heads][128] rows; only the tokens may be apart (slices of a packed
+    projection)."""
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
+    at = t.get_device()
+    if at != dev:
+        _wrong_device(at, dev, name)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens][heads][{HEAD_DIM}], got {list(t.shape)}")
+    n, heads, d = t.shape
+    s0, s1, s2 = t.stride()
+    if d != HEAD_DIM or s2 != 1 or (s1 != HEAD_DIM and heads > 1):
+        raise ValueError(f"{name} must be [tokens][heads][{HEAD_DIM}] with each token's heads contiguous, got "
+                         f"{list(t.shape)} with strides {list(t.stride())}")
     # a single token has no next one; torch may give it any stride
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * HEAD_DIM
+    return t.data_ptr(), n, heads, s0 if n > 1 else heads * HEAD_DIM
 
 
-def _positions(pos: Optional[torch.Tensor], axes: int, n: int, name: str):
+def _positions(pos: Optional[torch.Tensor], axes: int, n: int, dev: int, name: str) -> int:
     if pos is None:
-        return None
-    _expect(pos, torch.int32, name)
+        return 0
     if pos.numel() != axes * n or pos.shape[-1] != n:
         raise ValueError(f"{name} must be [{axes}][{n}], got {list(pos.shape)}")
-    return _addr(pos)
+    return _at(pos, torch.int32, dev, name)
 
 
-def _same_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
-    """Every tensor on one device, which is the current one: the library launches there."""
-    dev = first.get_device()
-    if dev < 0:
-        raise ValueError("dynamic_block_sparse_dsa_b200 works on CUDA tensors only (no CPU path)")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"the tensors of one call are on cuda:{dev} and on device {t.get_device()}")
-
-
-def _append_rope(fn: str, c, cache, seqs: SeqBatch, cu_new, k_new, v_new, kc_new, rope, pos_new, queries, q, pos_q, q_out,
+def _append_rope(fn: str, cache, seqs: SeqBatch, cu_new, k_new, v_new, kc_new, rope, pos_new, queries, q, pos_q, q_out,
                  dev_err, stream):
-    hkv, axes = cache.num_kv_heads, 1 if rope is None else rope.num_axes
-    total = 0 if k_new is None else k_new.shape[0]
-    fresh = _lib.NewTokensC()
-    if total:
-        k, ks = _rows(k_new, hkv, "k_new")
-        v, vs = _rows(v_new, hkv, "v_new")
-        _expect(cu_new, torch.int32, "cu_new")
-        if v_new.shape[0] != total or cu_new.numel() != seqs.seq_lens.numel() + 1:
-            raise ValueError("v_new must have k_new's tokens, cu_new one entry more than there are sequences")
-        if kc_new is not None and (kc_new.element_size() != 1 or tuple(kc_new.shape) != (total, cache.kc_pool.shape[1])):
-            raise ValueError(f"kc_new must hold one byte per element, [{total}][{cache.kc_pool.shape[1]}]")
-        fresh = _lib.NewTokensC(_addr(cu_new), total, k, v, ks, vs, None if kc_new is None else _addr(kc_new),
-                                _positions(pos_new, axes, total, "pos_new"))
+    lib = load()
+    dev = _current(cache.k_pool)
+    axes = 1 if rope is None else rope.num_axes
+    fresh = _NOTHING_NEW
+    if k_new is not None and len(k_new):
+        k, total, heads, ks = _rows(k_new, dev, "k_new")
+        v, v_total, v_heads, vs = _rows(v_new, dev, "v_new")
+        if heads != cache.num_kv_heads or v_heads != heads or v_total != total:
+            raise ValueError(f"k_new and v_new must be [{total}][{cache.num_kv_heads}][{HEAD_DIM}]")
+        if cu_new.numel() != seqs.seq_lens.numel() + 1:
+            raise ValueError("cu_new must have one entry more than there are sequences")
+        kc = 0
+        if kc_new is not None:
+            if kc_new.element_size() != 1 or kc_new.shape != (total, cache.kc_pool.shape[1]):
+                raise ValueError(f"kc_new must hold one byte per element, [{total}][{cache.kc_pool.shape[1]}]")
+            kc = _at(kc_new, kc_new.dtype, dev, "kc_new")
+        fresh = _lib.pack_new_tokens(_at(cu_new, torch.int32, dev, "cu_new"), total, k, v, ks, vs, kc,
+                                     _positions(pos_new, axes, total, dev, "pos_new"))
     rows = qc = None
     if q is not None:
         if rope is None or queries is None:
             raise ValueError("rotating queries needs rope and queries")
-        qp, qs = _rows(q, None, "q")
-        if q.shape[0] != queries.total_q:
-            raise ValueError(f"q has {q.shape[0]} rows for {queries.total_q} queries")
+        qp, n, heads, qs = _rows(q, dev, "q")
+        if n != queries.total_q:
+            raise ValueError(f"q has {n} rows for {queries.total_q} queries")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _expect(q_out, torch.bfloat16, "q_out")
-        if q_out.shape != q.shape:
+            with _on(stream):
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
-        rows = _lib.QueryRowsC(qp, qs, q.shape[1], _positions(pos_q, axes, q.shape[0], "pos_q"), _addr(q_out))
-        qc = queries.ctype()
-    _same_device(cache.k_pool, cache.v_pool, cache.kc_pool, seqs.block_table, seqs.seq_lens,
-                 *((cu_new, k_new, v_new, kc_new, pos_new) if total else ()),
-                 *((q, q_out, pos_q, queries.q_pos) if q is not None else ()),
-                 *(() if rope is None else (rope.inv_freq, rope.pair_axis)), dev_err)
-    s, r = seqs.ctype(), None if rope is None else rope.ctype()
-    _lib.check(fn, getattr(load(), fn)(
-        ctypes.byref(c), ctypes.byref(s), ctypes.byref(fresh), None if r is None else ctypes.byref(r),
-        None if qc is None else ctypes.byref(qc), None if rows is None else ctypes.byref(rows), _ptr(dev_err),
-        _stream(stream)))
+        rows = _lib.pack_query_rows(qp, qs, heads, _positions(pos_q, axes, n, dev, "pos_q"),
+                                    _at(q_out, torch.bfloat16, dev, "q_out"))
+        qc = queries.packed(dev)
+    rc = getattr(lib, fn)(cache.packed(dev), seqs.packed(dev), fresh, None if rope is None else rope.packed(dev), qc,
+                          rows, None if dev_err is None else _at(dev_err, torch.int32, dev, "dev_err"),
+                          _raw_stream(stream, dev))
+    if rc:
+        _lib.check(fn, rc)
     return q_out
+
+
+_NOTHING_NEW = _lib.pack_new_tokens(0, 0, 0, 0, 0, 0, 0, 0)
 
 
 def kv_append_rope(cache: PagedKVCache, seqs: SeqBatch, cu_new: Optional[torch.Tensor], k_new: Optional[torch.Tensor],
@@ -310,8 +371,8 @@ def kv_append_rope(cache: PagedKVCache, seqs: SeqBatch, cu_new: Optional[torch.T
     is appended, only the queries are rotated."""
     if not isinstance(cache, PagedKVCache):
         raise TypeError("kv_append_rope appends to a PagedKVCache (kv_append_fp8 to a PagedKVCacheFP8)")
-    return _append_rope("dsa_kv_append_rope", cache.ctype(), cache, seqs, cu_new, k_new, v_new, kc_new, rope, pos_new,
-                        queries, q, pos_q, q_out, dev_err, stream)
+    return _append_rope("dsa_kv_append_rope", cache, seqs, cu_new, k_new, v_new, kc_new, rope, pos_new, queries, q,
+                        pos_q, q_out, dev_err, stream)
 
 
 def kv_append_fp8(cache: PagedKVCacheFP8, seqs: SeqBatch, cu_new: Optional[torch.Tensor],
@@ -326,9 +387,8 @@ def kv_append_fp8(cache: PagedKVCacheFP8, seqs: SeqBatch, cu_new: Optional[torch
     it; the tile's earlier codes are then rounded anew."""
     if not isinstance(cache, PagedKVCacheFP8):
         raise TypeError("kv_append_fp8 appends to a PagedKVCacheFP8")
-    _same_device(cache.k_pool, cache.k_scale, cache.v_scale)
-    return _append_rope("dsa_kv_append_fp8", cache.ctype(), cache, seqs, cu_new, k_new, v_new, kc_new, rope, pos_new,
-                        queries, q, pos_q, q_out, dev_err, stream)
+    return _append_rope("dsa_kv_append_fp8", cache, seqs, cu_new, k_new, v_new, kc_new, rope, pos_new, queries, q,
+                        pos_q, q_out, dev_err, stream)
 
 
 def index_score(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, q_idx: torch.Tensor,
@@ -546,25 +606,27 @@ def sparse_attn_prefill(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch
     return out, lse
 
 
-def _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, dev_err):
+def _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, stream):
+    """(device, out, lse, the C calls' arguments up to lse)."""
     if not isinstance(cache, PagedKVCacheFP8):
         raise TypeError("the fp8 attention calls read a PagedKVCacheFP8")
-    _expect(q, torch.bfloat16, "q")
-    _expect(sel, torch.int32, "sel")
-    _expect(cnt, torch.int32, "cnt")
+    dev = _current(cache.k_pool)
     T = queries.total_q
     if q.dim() != 3 or q.shape[0] != T or q.shape[2] != HEAD_DIM:
         raise ValueError(f"q must be [{T}][heads][{HEAD_DIM}], got {list(q.shape)}")
     if sel.dim() != 2 or sel.shape[0] != T or cnt.numel() != T:
         raise ValueError(f"sel must be [{T}][k_max] and cnt [{T}]")
-    out, lse = _attn_out(q, out, lse)
-    _expect(out, torch.bfloat16, "out")
-    _expect(lse, torch.float32, "lse")
-    if out.shape != q.shape or lse.shape != q.shape[:2]:
+    if out is None or lse is None:
+        with _on(stream):
+            out, lse = _attn_out(q, out, lse)
+    rows = q.shape
+    if out.shape != rows or lse.shape != rows[:2]:
         raise ValueError("out must have q's shape and lse its first two dimensions")
-    _same_device(cache.k_pool, cache.v_pool, cache.k_scale, cache.v_scale, seqs.block_table, seqs.seq_lens,
-                 queries.cu_q, queries.q_pos, q, sel, cnt, out, lse, dev_err)
-    return out, lse, 1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else float(sm_scale)
+    return dev, out, lse, (
+        cache.packed(dev), seqs.packed(dev), queries.packed(dev), _at(q, torch.bfloat16, dev, "q"), rows[1],
+        _at(sel, torch.int32, dev, "sel"), _at(cnt, torch.int32, dev, "cnt"), sel.shape[1],
+        1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else float(sm_scale), _at(out, torch.bfloat16, dev, "out"),
+        _at(lse, torch.float32, dev, "lse"))
 
 
 def sparse_attn_decode_fp8(cache: PagedKVCacheFP8, seqs: SeqBatch, queries: QueryBatch, q: torch.Tensor,
@@ -572,16 +634,17 @@ def sparse_attn_decode_fp8(cache: PagedKVCacheFP8, seqs: SeqBatch, queries: Quer
                            workspace: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
                            stream=None):
     """sparse_attn_decode over the 8-bit cache: (out bf16, lse fp32), same workspace."""
-    out, lse, scale = _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, dev_err)
+    lib = load()
+    dev, out, lse, args = _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, stream)
     if workspace is None:
-        workspace = torch.zeros(decode_workspace_size(queries.total_q, q.shape[1], cache.num_kv_heads, sel.shape[1]),
-                                dtype=torch.uint8, device=q.device)
-    _same_device(q, workspace)
-    c, s, qq = cache.ctype(), seqs.ctype(), queries.ctype()
-    _lib.check("dsa_sparse_attn_decode_fp8", load().dsa_sparse_attn_decode_fp8(
-        ctypes.byref(c), ctypes.byref(s), ctypes.byref(qq), _ptr(q), q.shape[1], _ptr(sel), _ptr(cnt),
-        sel.shape[1], scale, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _ptr(dev_err), _stream(stream)))
+        with _on(stream):
+            workspace = torch.zeros(decode_workspace_size(queries.total_q, q.shape[1], cache.num_kv_heads,
+                                                          sel.shape[1]), dtype=torch.uint8, device=q.device)
+    rc = lib.dsa_sparse_attn_decode_fp8(
+        *args, _at(workspace, workspace.dtype, dev, "workspace"), workspace.numel() * workspace.element_size(),
+        None if dev_err is None else _at(dev_err, torch.int32, dev, "dev_err"), _raw_stream(stream, dev))
+    if rc:
+        _lib.check("dsa_sparse_attn_decode_fp8", rc)
     return out, lse
 
 
@@ -589,11 +652,12 @@ def sparse_attn_prefill_fp8(cache: PagedKVCacheFP8, seqs: SeqBatch, queries: Que
                             sel: torch.Tensor, cnt: torch.Tensor, sm_scale: Optional[float] = None, out=None,
                             lse=None, dev_err: Optional[torch.Tensor] = None, stream=None):
     """sparse_attn_prefill over the 8-bit cache: (out bf16, lse fp32)."""
-    out, lse, scale = _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, dev_err)
-    c, s, qq = cache.ctype(), seqs.ctype(), queries.ctype()
-    _lib.check("dsa_sparse_attn_prefill_fp8", load().dsa_sparse_attn_prefill_fp8(
-        ctypes.byref(c), ctypes.byref(s), ctypes.byref(qq), _ptr(q), q.shape[1], _ptr(sel), _ptr(cnt),
-        sel.shape[1], scale, _ptr(out), _ptr(lse), _ptr(dev_err), _stream(stream)))
+    lib = load()
+    dev, out, lse, args = _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, stream)
+    rc = lib.dsa_sparse_attn_prefill_fp8(
+        *args, None if dev_err is None else _at(dev_err, torch.int32, dev, "dev_err"), _raw_stream(stream, dev))
+    if rc:
+        _lib.check("dsa_sparse_attn_prefill_fp8", rc)
     return out, lse
 
 

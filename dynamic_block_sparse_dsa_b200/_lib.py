@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -56,14 +57,23 @@ class QueryRowsC(ctypes.Structure):
     _fields_ = [("q", c_vp), ("q_stride", ctypes.c_int64), ("num_heads", c_i32), ("pos", c_vp), ("out", c_vp)]
 
 
+# The same structs as packed bytes, for the calls that take them as plain
+# pointers: packing costs a fifth of filling a ctypes structure.
+pack_cache = struct.Struct("@PPPiiiii").pack
+pack_cache_fp8 = struct.Struct("@PPPPPiiiii").pack
+pack_seqs = struct.Struct("@PiPi").pack
+pack_queries = struct.Struct("@PPi").pack
+pack_rope = struct.Struct("@PPiiif").pack
+pack_new_tokens = struct.Struct("@PiPPqqPP").pack
+pack_query_rows = struct.Struct("@PqiPP").pack
+
+
 # exported symbol -> (argtypes, restype); mirrors include/dsa.h
 P = ctypes.POINTER
 SIGNATURES = {
     "dsa_kv_append": ([P(KvCacheC), P(SeqsC), c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp], c_i32),
-    "dsa_kv_append_rope": ([P(KvCacheC), P(SeqsC), P(NewTokensC), P(RopeC), P(QueriesC), P(QueryRowsC), c_vp, c_vp],
-                           c_i32),
-    "dsa_kv_append_fp8": ([P(KvCacheFp8C), P(SeqsC), P(NewTokensC), P(RopeC), P(QueriesC), P(QueryRowsC), c_vp, c_vp],
-                          c_i32),
+    "dsa_kv_append_rope": ([c_vp] * 8, c_i32),
+    "dsa_kv_append_fp8": ([c_vp] * 8, c_i32),
     "dsa_index_score": ([P(KvCacheC), P(SeqsC), P(QueriesC), c_vp, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp],
                         c_i32),
     "dsa_topk_blocks": ([P(SeqsC), P(QueriesC), c_vp, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp], c_i32),
@@ -83,9 +93,9 @@ SIGNATURES = {
                                  ctypes.c_float, c_vp, c_vp, c_vp, c_vp], c_i32),
     "dsa_sparse_attn_decode_noalloc": ([P(KvCacheC), P(SeqsC), P(QueriesC), c_vp, c_i32, c_vp, c_vp, c_i32,
                                         ctypes.c_float, c_vp, c_vp, c_vp, c_vp], c_i32),
-    "dsa_sparse_attn_decode_fp8": ([P(KvCacheFp8C), P(SeqsC), P(QueriesC), c_vp, c_i32, c_vp, c_vp, c_i32,
+    "dsa_sparse_attn_decode_fp8": ([c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_i32,
                                     ctypes.c_float, c_vp, c_vp, c_vp, ctypes.c_size_t, c_vp, c_vp], c_i32),
-    "dsa_sparse_attn_prefill_fp8": ([P(KvCacheFp8C), P(SeqsC), P(QueriesC), c_vp, c_i32, c_vp, c_vp, c_i32,
+    "dsa_sparse_attn_prefill_fp8": ([c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_i32,
                                      ctypes.c_float, c_vp, c_vp, c_vp, c_vp], c_i32),
     "dsa_decode_fused_workspace_size": ([c_i32, c_i32, c_i32, c_i32], ctypes.c_size_t),
     "dsa_decode_fused": ([P(KvCacheC), P(SeqsC), P(QueriesC), c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32,

@@ -137,31 +137,43 @@ void attn_schedule(AttnArgs &a, bool allow_split, bool allow_cluster = false) {
     a.interleave = (a.pair_aligned && a.num_kv_heads > 1) ? 1 : 0;
 }
 
-// Work split of the E4M3 attention kernel; returns the grid.  Whole rounds of
-// one pair per warp as long as there are pairs for every warp; the pairs left
-// over are split over the CTAs, by tiles where partial states have a workspace,
-// else by whole pairs.  A pair of few tiles is not worth a merge of eight warps:
-// its left-over round runs a pair per warp as well.
-int attn_schedule_fp8(AttnArgs &a, bool allow_split) {
+// Work split of the E4M3 attention kernel (see AttnArgs::warp_rounds): whole
+// rounds of one pair per warp while there are pairs for every warp, then teams
+// for the pairs left over.
+void attn_schedule_fp8(AttnArgs &a, bool allow_split) {
     long long C = sm_count();
     if (C > kAttnMaxCtas) C = kAttnMaxCtas;
-    const long long pairs = (long long)a.total_q * a.num_kv_heads, W = C * kFp8Warps;
+    const long long pairs = (long long)a.total_q * a.num_kv_heads;
+    // 12 warps hide more latency where every warp has a pair of its own (4096-query
+    // chunk 2.63 ms, 333 queries 113 us; with 8 warps 3.00 ms, 125 us); 8 divide a
+    // decode batch better (8 long contexts 11.6 us, 64 short ones 26.5 us; with 12
+    // warps 12.7 us, 29.5 us)
+    const int warps = pairs < C * fp8_max_warps(1) || a.group > 8 ? 8 : fp8_max_warps(1);
+    const long long W = C * warps;
+    a.warps = warps;
     const long long tiles = (long long)a.k_max << a.tile_shift;
     a.warp_rounds = (int)(pairs / W);
-    long long left = pairs - a.warp_rounds * W;
-    if (left > 0 && tiles < kFp8Warps) {
+    const long long left = pairs - a.warp_rounds * W;
+    a.team = 0;
+    a.splits = 1;
+    a.num_ctas = (int)C;
+    if (left == 0) return;
+    // the largest team that leaves one for every pair, and a tile for every warp
+    int team = 1;
+    for (int t = 2; t <= warps; ++t)
+        if (warps % t == 0 && left * t <= W && t <= tiles) team = t;
+    if (team == 1) {
         ++a.warp_rounds;
-        left = 0;
+    } else {
+        a.team = team;
+        // fewer than half as many pairs as CTAs: several CTAs a pair, each with a tile for every warp
+        if (allow_split && a.warp_rounds == 0 && team == warps) {
+            long long s = C / left;
+            if (s > tiles / warps) s = tiles / warps;
+            a.splits = s > 1 ? (int)s : 1;
+        }
     }
-    a.pair_aligned = allow_split ? 0 : 1;
-    a.total_units = left * tiles;
-    long long share = allow_split ? a.total_units : left;
-    if (share > C) share = C;
-    if (share > left * 60) share = left * 60;   // the kernel merges <= 63 partials of a pair
-    a.num_ctas = share > 0 ? (int)share : 1;
-    if (a.warp_rounds == 0) return a.num_ctas;
-    const long long full = (pairs + kFp8Warps - 1) / kFp8Warps;   // CTAs that have a pair for a warp
-    return (int)(full < C ? full : C);
+    if (pairs < W) a.num_ctas = a.splits > 1 ? (int)(left * a.splits) : (int)((left * team + warps - 1) / warps);
 }
 
 // Cache: dsa_kv_cache or dsa_kv_cache_fp8, already checked (the caller sets the scales)
@@ -743,8 +755,8 @@ int dsa_sparse_attn_decode_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *se
     char *ws = static_cast<char *>(workspace);
     a.counters = reinterpret_cast<int32_t *>(ws + L.counters);
     a.part = reinterpret_cast<float *>(ws + L.part);
-    const int ctas = attn_schedule_fp8(a, true);
-    return from_cuda(launch_sparse_attn_fp8(a, ctas, reinterpret_cast<cudaStream_t>(stream)));
+    attn_schedule_fp8(a, true);
+    return from_cuda(launch_sparse_attn_fp8(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int dsa_sparse_attn_prefill_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *seqs, const dsa_queries *queries,
@@ -755,8 +767,8 @@ int dsa_sparse_attn_prefill_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *s
     int rc = attn_common_fp8(cache, seqs, queries, q, num_q_heads, sel, cnt, k_max, sm_scale, out, lse, dev_err, a);
     if (rc) return rc;
     if (queries->total_q == 0) return DSA_OK;
-    const int ctas = attn_schedule_fp8(a, false);   // whole pairs: no partial states, no workspace
-    return from_cuda(launch_sparse_attn_fp8(a, ctas, reinterpret_cast<cudaStream_t>(stream)));
+    attn_schedule_fp8(a, false);   // no pair over several CTAs: no partial states, no workspace
+    return from_cuda(launch_sparse_attn_fp8(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -178,9 +178,11 @@ struct AttnArgs {
     // no workspace is touched
     int cluster2;
     // E4M3 kernel: every warp runs warp_rounds whole pairs by itself (pairs r =
-    // warp + i * warps of the KV-head-major order r = kvh * T + t, i < warp_rounds);
-    // total_units, num_ctas and pair_aligned then describe the pairs behind them
-    int warp_rounds;
+    // warp + i * warps of the KV-head-major order r = kvh * T + t, i < warp_rounds).
+    // The pairs behind them: none (team 0), one per team of `team` warps of a CTA
+    // (a divisor of its warps), or, with splits > 1 (team is the whole CTA then), one per
+    // `splits` CTAs, each taking an equal part of the pair's tiles
+    int warps, warp_rounds, team, splits;   // warps per CTA
     float *part;             // [2*C][group][kAttnPartStride] partial (o[128], m, l) of split pairs
     int32_t *counters;       // [T*Hkv] units merged so far per split pair
     int32_t *dev_err;
@@ -230,8 +232,7 @@ cudaError_t launch_select_blocks(const SelectArgs &a, cudaStream_t stream);
 int topk_max_blocks();   // longest block table the standalone Top-K kernel accepts
 // the K/V pool and Q tensor maps are built by the launcher from AttnArgs
 cudaError_t launch_sparse_attn(const AttnArgs &a, cudaStream_t stream);
-// `ctas`: the grid (a.num_ctas of them share the pairs behind the warps' own)
-cudaError_t launch_sparse_attn_fp8(const AttnArgs &a, int ctas, cudaStream_t stream);
+cudaError_t launch_sparse_attn_fp8(const AttnArgs &a, cudaStream_t stream);   // grid: a.num_ctas
 cudaError_t launch_decode_fused(const AttnArgs &a, const FusedArgs &f, cudaStream_t stream);
 // host-side checks of dsa_sparse_attn_decode's arguments, without any CUDA
 // call: DSA_OK or the status the entry point would return
@@ -240,8 +241,9 @@ int check_decode_attn_args(const dsa_kv_cache *cache, const dsa_seqs *seqs, cons
                            int32_t k_max, float sm_scale, void *out, float *lse);
 // largest grid the attention kernel uses (sizes the partial-state workspace)
 constexpr int kAttnMaxCtas = 256;
-// warps per CTA of the E4M3 attention kernel
-constexpr int kFp8Warps = 8;
+// most warps per CTA of the E4M3 attention kernel, for nt tiles of 8 query heads: as
+// many as the registers allow (168 and 255 a thread)
+constexpr int fp8_max_warps(int nt) { return nt == 1 ? 12 : 8; }
 // floats per partial-state row: o[128], m, l, padded to a 16-byte multiple
 constexpr int kAttnPartStride = 132;
 

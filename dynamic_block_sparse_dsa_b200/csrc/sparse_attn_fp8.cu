@@ -26,10 +26,10 @@
 // The 8-bit operands reach the fragments without byte shuffles of K: an
 // ldmatrix lane holds four neighbouring dims of one token, which serve as the
 // k indexes (2c, 2c+1) and (2c+8, 2c+9) of one mma when the query fragments are
-// laid out the same way.  For V the transposing ldmatrix moves byte pairs, so
-// a lane holds dims (2g, 2g+1) of tokens 2c and 2c+1; one byte permutation per
-// register makes them the rows g and g+8 of V^T, i.e. accumulator rows g and
-// g+8 of a 16-dim group are its dims 2g and 2g+1.
+// laid out the same way.  For V the transposing 8-bit ldmatrix gives a lane four
+// rows of one column; the rows' addresses are permuted so that these are the
+// tokens 2c, 2c+1, 2c+8 and 2c+9 of the column's dim, again the k indexes of one
+// mma (of the weights as the 16-bit transpose leaves them).
 //
 // Feeding.  Every warp is its own producer: it holds a ring of kSlots 8-KiB
 // slots for K and V tiles in turn and issues the TMA box of its next tile as
@@ -42,11 +42,12 @@
 // rounds give each warp a pair of its own, which it writes out by itself; the
 // pairs go KV-head-major, so that all warps read one KV head's slice of the
 // pool at a time and the queries that select the same block find it in L2.
-// The pairs left over (all of a decode batch) are split by tiles: CTA c takes
-// a contiguous range of (pair, tile) units, its warps every kWarps-th of them,
-// and the warps' softmax states merge through shared memory.  A pair split
-// over CTAs leaves partial states in the workspace, and the CTA that completes
-// the pair's count merges them (nobody waits).
+// The pairs left over (all of a decode batch) go to teams of several warps of
+// one CTA, the largest that still leave a team for every pair: a team's warps
+// take the pair's tiles in turn and merge their softmax states through shared
+// memory.  With less than half as many pairs as CTAs, the tiles of a pair are
+// split over several CTAs; their states meet in the workspace, and the CTA that
+// completes the pair's count merges them (nobody waits).
 // All waits are bounded (DSA_DEV_ERR_WAIT on timeout, no hang).
 #include "dsa_kernels.h"
 #include "dsa_tma.cuh"
@@ -60,26 +61,25 @@ namespace dsa {
 namespace {
 
 constexpr int kTileBytes = kBlockSize * kHeadDim;   // 8 KiB: 64 rows x 128 codes
-constexpr int kWarps = kFp8Warps;
-constexpr int kThreads = kWarps * 32;
-constexpr int kSlots = 2;
+constexpr int kSlots = 2;                           // per warp: a K tile and a V tile
+constexpr int kRingBytes = kSlots * kTileBytes;
 constexpr int kMergeStride = 132;                   // floats per merge row (padded against bank conflicts)
 constexpr int kMaxSmemSeqs = 256;                   // cu_q entries cached in shared memory
-constexpr int kMaxSplitSlots = 63;                  // most CTAs whose ranges cover one pair (the host caps it at 60)
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int NT>
+// shared memory: the rings (a warp's ring takes its state in the merge, when its
+// last tile is read), then the rest
 struct Plan {
-    static constexpr int kRows = 8 * NT;
-    static constexpr int kOffMergeO = kWarps * kSlots * kTileBytes;
-    static constexpr int kOffMergeML = kOffMergeO + kWarps * kRows * kMergeStride * 4;   // [warp][row] (m, l)
-    static constexpr int kOffRb = kOffMergeML + kWarps * kRows * 8;                      // range begin of every CTA
-    static constexpr int kOffCuq = kOffRb + (kAttnMaxCtas + 1) * 4 + 4;
-    static constexpr int kOffBars = (kOffCuq + (kMaxSmemSeqs + 1) * 4 + 7) / 8 * 8;
-    static constexpr int kOffWords = kOffBars + kWarps * kSlots * 8;                     // abort, last
-    static constexpr int kSmemBytes = kOffWords + 8 + 1024;                              // + base alignment slack
-    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+    int ml, cuq, bars, words, bytes;
+    __host__ __device__ constexpr explicit Plan(int warps)
+        : ml(warps * kRingBytes),                              // [warp][16] (m, l)
+          cuq(ml + warps * 16 * 8),
+          bars((cuq + (kMaxSmemSeqs + 1) * 4 + 7) / 8 * 8),
+          words(bars + warps * kSlots * 8),                    // never, last
+          bytes(words + 8 + 1024) {}                           // + base alignment slack
 };
+static_assert(Plan(fp8_max_warps(1)).bytes <= 227 * 1024, "shared memory");
+static_assert(16 * kMergeStride * 4 <= kRingBytes, "a warp's state fits its ring");
 
 using unit_t = uint32_t;
 
@@ -89,6 +89,16 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
         "{%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// two 16x16 byte matrices, transposed: lane (g, c) gets bytes of rows 4c .. 4c+3
+// of column g (r0; r2 of the second matrix) and of column g + 8 (r1; r3).  Lane
+// i gives the address of row i (16 + i: the second matrix).
+__device__ __forceinline__ void ldmatrix_b8_x2_trans(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2,
+                                                     uint32_t &r3) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr));
 }
 
 // four E4M3 codes -> two pairs of f16 (exact)
@@ -178,7 +188,7 @@ __device__ __forceinline__ void load_queries(const __nv_bfloat16 *q, int group, 
     }
 }
 
-// A warp's running state for one pair: O^T accumulators of dims 16 dm + 2 g (+1) x
+// A warp's running state for one pair: O^T accumulators of dims 16 dm + g (+8) x
 // heads 8 nt + 2 cq (+1), and per head the maximum and this lane's part of the sum
 template <int NT>
 struct State {
@@ -292,35 +302,33 @@ template <int NT>
 __device__ __forceinline__ void weigh(uint32_t tv, float s_v, const uint32_t (&pb)[4][NT][2],
                                       const float (&alpha)[NT][2], State<NT> &st) {
     const int lane = threadIdx.x & 31;
-    const int lr = lane & 15, lc = lane >> 4;
+    // the token whose row this lane addresses: row 4 c + i of a matrix is token
+    // 2 c + (i & 1) + 8 (i >> 1) of its 16
+    const int r = lane & 15, tok = (lane & 16) + 2 * (r >> 2) + (r & 1) + 8 * ((r >> 1) & 1);
 #pragma unroll
-    for (int dg = 0; dg < 4; ++dg) {   // 32 dims: two groups of 16 per ldmatrix
-        float pv[2][NT][4];
+    for (int dm = 0; dm < 8; ++dm) {
+        float pv[NT][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int nt = 0; nt < NT; ++nt) pv[nt][0] = pv[nt][1] = pv[nt][2] = pv[nt][3] = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) pv[i][nt][0] = pv[i][nt][1] = pv[i][nt][2] = pv[i][nt][3] = 0.f;
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
+        for (int mp = 0; mp < 2; ++mp) {   // 32 tokens: two k-steps per ldmatrix
             uint32_t w[4], a0[4], a1[4];
-            ldmatrix_x4_trans(tv + swz128(16 * mt + lr, 2 * dg + lc), w[0], w[1], w[2], w[3]);
-            codes_to_f16(__byte_perm(w[0], 0u, 0x3120), a0[0], a0[1]);
-            codes_to_f16(__byte_perm(w[1], 0u, 0x3120), a0[2], a0[3]);
-            codes_to_f16(__byte_perm(w[2], 0u, 0x3120), a1[0], a1[1]);
-            codes_to_f16(__byte_perm(w[3], 0u, 0x3120), a1[2], a1[3]);
+            ldmatrix_b8_x2_trans(tv + swz128(32 * mp + tok, dm), w[0], w[1], w[2], w[3]);
+            codes_to_f16(w[0], a0[0], a0[2]);
+            codes_to_f16(w[1], a0[1], a0[3]);
+            codes_to_f16(w[2], a1[0], a1[2]);
+            codes_to_f16(w[3], a1[1], a1[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                mma_f16_16816(pv[0][nt], a0, pb[mt][nt][0], pb[mt][nt][1]);
-                mma_f16_16816(pv[1][nt], a1, pb[mt][nt][0], pb[mt][nt][1]);
+                mma_f16_16816(pv[nt], a0, pb[2 * mp][nt][0], pb[2 * mp][nt][1]);
+                mma_f16_16816(pv[nt], a1, pb[2 * mp + 1][nt][0], pb[2 * mp + 1][nt][1]);
             }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    st.o[2 * dg + i][nt][k] = fmaf(pv[i][nt][k], s_v, st.o[2 * dg + i][nt][k] * alpha[nt][k & 1]);
+            for (int k = 0; k < 4; ++k)
+                st.o[dm][nt][k] = fmaf(pv[nt][k], s_v, st.o[dm][nt][k] * alpha[nt][k & 1]);
     }
 }
 
@@ -328,27 +336,25 @@ __device__ __forceinline__ void weigh(uint32_t tv, float s_v, const uint32_t (&p
 struct Tile {
     int x;   // < 0: the stream has ended
     int blk, row, kvh;
-    float s_k, s_v;
 };
 
 }  // namespace
 
 // NT: query-head n-tiles of 8 (the GQA group is <= 8 * NT)
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(fp8_max_warps(NT) * 32, 1)
 sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, AttnArgs a) {
-    using P = Plan<NT>;
+    const int threads = blockDim.x, warps = threads >> 5;
+    const Plan plan(warps);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (base - raw);
-    float *s_mo = reinterpret_cast<float *>(gbase + P::kOffMergeO);    // [warp][kRows][kMergeStride]
-    float *s_ml = reinterpret_cast<float *>(gbase + P::kOffMergeML);   // [warp][kRows][2]
-    unit_t *s_rb = reinterpret_cast<unit_t *>(gbase + P::kOffRb);
-    int *s_cuq = reinterpret_cast<int *>(gbase + P::kOffCuq);
-    volatile int *s_never = reinterpret_cast<volatile int *>(gbase + P::kOffWords);   // stays 0: no abort flag
+    float *s_ml = reinterpret_cast<float *>(gbase + plan.ml);   // [warp][16][2]
+    int *s_cuq = reinterpret_cast<int *>(gbase + plan.cuq);
+    volatile int *s_never = reinterpret_cast<volatile int *>(gbase + plan.words);   // stays 0: no abort flag
     volatile int *s_last = s_never + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
-    const uint32_t ring = base + warp * kSlots * kTileBytes, bars = base + P::kOffBars + warp * kSlots * 8;
+    const uint32_t ring = base + warp * kRingBytes, bars = base + plan.bars + warp * kSlots * 8;
     const int G = a.group, T = a.total_q;
     const unit_t K = (unit_t)a.k_max << a.tile_shift;   // tiles per pair
 
@@ -363,29 +369,35 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             prefetch_tensormap(&tm_v);
         }
     }
-    // the left-over pairs' units, split over the first num_ctas CTAs
-    const unit_t tail_units = (unit_t)a.total_units;
-    const unit_t up = a.pair_aligned ? K : 1;
-    for (int i = tid; i <= a.num_ctas; i += kThreads)
-        s_rb[i] = (unit_t)((unsigned long long)i * (tail_units / up) / (unsigned)a.num_ctas) * up;
     const bool cached = a.num_seqs + 1 <= kMaxSmemSeqs;
     if (cached)
-        for (int i = tid; i <= a.num_seqs; i += kThreads) s_cuq[i] = __ldg(a.cu_q + i);
+        for (int i = tid; i <= a.num_seqs; i += threads) s_cuq[i] = __ldg(a.cu_q + i);
     __syncthreads();
 
-    const unit_t u0 = c < a.num_ctas ? s_rb[c] : tail_units, u1 = c < a.num_ctas ? s_rb[c + 1] : tail_units;
-    const int W = gridDim.x * kWarps;
-    const unit_t n_own = (unit_t)a.warp_rounds * K;     // this warp's stream: tiles of its own pairs, then
-    const unit_t n_all = n_own + (u1 - u0 > (unit_t)warp ? (u1 - u0 - warp + kWarps - 1) / kWarps : 0);   // its share
-    const int own0 = c * kWarps + warp, tail0 = a.warp_rounds * W;
-    const int pairs = T * a.num_kv_heads;
+    const int W = gridDim.x * warps, pairs = T * a.num_kv_heads;
+    const int own0 = c * warps + warp;                 // this warp's own pairs: own0 + i * W
+    const unit_t n_own = (unit_t)a.warp_rounds * K;     // the warp's stream: their tiles, then its share
+    // of a team's pair: tiles j_first, j_first + team, ... of the CTA's part [j_lo, j_hi)
+    const int team = a.team, splits = a.splits, member = team > 0 ? warp % team : 0;
+    int tail_pair = -1;
+    unit_t j_lo = 0, j_hi = 0;
+    if (team > 0) {
+        const int i = splits > 1 ? c / splits : own0 / team;
+        if (a.warp_rounds * W + i < pairs) {
+            tail_pair = a.warp_rounds * W + i;
+            const unit_t part = splits > 1 ? (unit_t)(c - i * splits) : 0u;
+            j_lo = part * K / (unit_t)splits;
+            j_hi = (part + 1) * K / (unit_t)splits;
+        }
+    }
+    const unit_t j_first = j_lo + (unit_t)member;
+    const unit_t n_all = n_own + (j_hi > j_first ? (j_hi - j_first + team - 1) / team : 0);
 
     // ---- the stream: 32 places at a time are resolved to pool rows, a lane each
     uint32_t err_bits = 0;
     unsigned ready = 0;           // resolved places not yet taken
     int x_base = -32;
     int l_blk = 0, l_row = 0, l_kvh = 0;
-    float l_sk = 0.f, l_sv = 0.f;
     auto resolve = [&]() {
         const unit_t x = (unit_t)x_base + lane;
         bool good = false;
@@ -396,10 +408,8 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 pair = (unit_t)own0 + i * W;
                 ju = x - i * K;
             } else {
-                const unit_t u = u0 + warp + (x - n_own) * kWarps;
-                pair = u / K;
-                ju = u - pair * K;
-                pair += tail0;
+                pair = (unit_t)tail_pair;
+                ju = j_first + (x - n_own) * (unit_t)team;
             }
             if (pair < (unit_t)pairs) {
                 l_kvh = (int)(pair / (unit_t)T);
@@ -432,9 +442,6 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                             err_bits |= DSA_DEV_ERR_PAGE;
                         } else if (l_blk <= p >> 6) {   // tiles past the position (own block only) hold nothing visible
                             l_row = (pg << a.block_shift) + (sub << 6);
-                            const size_t i = (size_t)(l_row >> 6) * a.num_kv_heads + l_kvh;
-                            l_sk = ld_ordered_cg(a.k_scale + i);
-                            l_sv = ld_ordered_cg(a.v_scale + i);
                             good = true;
                         }
                     }
@@ -458,27 +465,32 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         d.blk = __shfl_sync(0xffffffffu, l_blk, src);
         d.row = __shfl_sync(0xffffffffu, l_row, src);
         d.kvh = __shfl_sync(0xffffffffu, l_kvh, src);
-        d.s_k = __shfl_sync(0xffffffffu, l_sk, src);
-        d.s_v = __shfl_sync(0xffffffffu, l_sv, src);
         return d;
     };
-    // ---- the ring: K tile i in slot 0, V tile i in slot 1
-    unsigned issued = 0, taken = 0;   // tiles of either kind
+    // ---- the ring: K and V tiles in turn, K of tile i the 2i-th copy, V the next;
+    // copy n goes to slot n % kSlots as soon as copy n - kSlots is read
+    int in_flight = 0, slot_in = 0, slot = 0;   // copies not yet waited for; next slot to fill, to read
+    uint32_t phase = 0;                         // of the slot to read
     auto issue = [&](const CUtensorMap *tm, const Tile &d) {
         if (d.x >= 0) {
             if (lane == 0) {
-                const int s = issued % kSlots;
-                mbar_arrive_expect_tx(bars + 8 * s, kTileBytes);
-                tma_load_3d(ring + s * kTileBytes, tm, 0, d.kvh, d.row, bars + 8 * s);
+                mbar_arrive_expect_tx(bars + 8 * slot_in, kTileBytes);
+                tma_load_3d(ring + slot_in * kTileBytes, tm, 0, d.kvh, d.row, bars + 8 * slot_in);
             }
-            ++issued;
+            slot_in = slot_in + 1 == kSlots ? 0 : slot_in + 1;
+            ++in_flight;
         }
     };
-    auto await = [&]() {
-        const int s = taken % kSlots;
-        const bool ok = mbar_wait(bars + 8 * s, (taken / kSlots) & 1, s_never);
-        if (ok) ++taken;
-        return __all_sync(0xffffffffu, ok) != 0;
+    uint32_t tile = 0;   // address of the copy waited for
+    auto arrived = [&]() {
+        if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * slot, phase, s_never))) return false;
+        tile = ring + slot * kTileBytes;
+        --in_flight;
+        if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1;
+        }
+        return true;
     };
 
     uint32_t qb[8][NT][2];
@@ -495,28 +507,31 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         while (!dead && cur.x >= 0 && (unit_t)cur.x < x_end) {
             float sc[4][NT][4], alpha[NT][2];
             uint32_t pb[4][NT][2];
-            if (!await()) { dead = true; break; }
-            scores<NT>(ring, qb, sc);
+            // one address for the whole warp; the values are used after the first product
+            const size_t si = (size_t)(cur.row >> 6) * a.num_kv_heads + cur.kvh;
+            const float s_k = ld_ordered_cg(a.k_scale + si), s_v = ld_ordered_cg(a.v_scale + si);
+            if (!arrived()) { dead = true; break; }
+            scores<NT>(tile, qb, sc);
             __syncwarp();
             issue(&tm_k, nxt);
             const int lim = p - cur.blk * kBlockSize;   // >= 63 but in the query's own tile
-            softmax<NT>(sc, mul, cur.s_k, lim, st, alpha, pb);
-            if (!await()) { dead = true; break; }
-            const uint32_t tv = ring + kTileBytes;
+            softmax<NT>(sc, mul, s_k, lim, st, alpha, pb);
+            const Tile after = next();
+            if (!arrived()) { dead = true; break; }
             if (lim < kBlockSize - 1) {
                 // slots past the query's position hold whatever the cache had there;
                 // a zero weight times a NaN is NaN, so their value rows are cleared
                 for (int e = lane; e < (kBlockSize - 1 - lim) * 8; e += 32)
-                    st_shared_zero16(tv + swz128(lim + 1 + (e >> 3), e & 7));
+                    st_shared_zero16(tile + swz128(lim + 1 + (e >> 3), e & 7));
                 __syncwarp();
             }
-            weigh<NT>(tv, cur.s_v, pb, alpha, st);
+            weigh<NT>(tile, s_v, pb, alpha, st);
             // generic-proxy stores (the cleared rows) before the TMA refills the slot
             if (lim < kBlockSize - 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             issue(&tm_v, nxt);
             cur = nxt;
-            nxt = next();
+            nxt = after;
         }
     };
 
@@ -534,110 +549,101 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const float inv[2] = {inv_of(st.l[nt][0]), inv_of(st.l[nt][1])};
-            const int h = 8 * nt + 2 * cq;
-            __nv_bfloat16 *dst = a.out + (row0 + h) * kHeadDim + 2 * g;
+            // neighbouring lanes g, g ^ 1 trade a head each: 4-byte stores of two dims
+            const int h = 8 * nt + 2 * cq + (g & 1);
+            __nv_bfloat16 *dst = a.out + (row0 + h) * kHeadDim + (g & ~1);
 #pragma unroll
-            for (int dm = 0; dm < 8; ++dm) {
-                const float *o = st.o[dm][nt];
-                if (h < G) *reinterpret_cast<uint32_t *>(dst + 16 * dm) = pack_bf16x2(o[0] * inv[0], o[2] * inv[0]);
-                if (h + 1 < G)
-                    *reinterpret_cast<uint32_t *>(dst + kHeadDim + 16 * dm) = pack_bf16x2(o[1] * inv[1], o[3] * inv[1]);
-            }
+            for (int dm = 0; dm < 8; ++dm)
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                    const float x = st.o[dm][nt][k] * inv[0], y = st.o[dm][nt][k + 1] * inv[1];
+                    const float other = __shfl_xor_sync(0xffffffffu, (g & 1) ? x : y, 4);
+                    const uint32_t v = (g & 1) ? pack_bf16x2(other, y) : pack_bf16x2(x, other);
+                    if (h < G) *reinterpret_cast<uint32_t *>(dst + 16 * dm + 4 * k) = v;
+                }
             if (a.lse && g < 2 && 8 * nt + 2 * cq + g < G)
                 a.lse[row0 + 8 * nt + 2 * cq + g] = lse_of(g ? st.m[nt][1] : st.m[nt][0], g ? st.l[nt][1] : st.l[nt][0]);
         }
     }
 
-    // ---- the CTA's share of the left-over pairs
-    for (unit_t u = u0; u < u1;) {
-        const unit_t tail_pair = u / K, seg_end = min(u1, (tail_pair + 1) * K);
-        const int pair = tail0 + (int)tail_pair;
-        const int kvh = pair / T, t = pair - kvh * T;
+    // ---- the team's pair (its warps agree on tail_pair)
+    if (tail_pair >= 0) {
+        const int kvh = tail_pair / T, t = tail_pair - kvh * T;
         const size_t row0 = (size_t)t * a.num_q_heads + (size_t)kvh * G;
-        const unit_t x_end = n_own + (seg_end - u0 > (unit_t)warp ? (seg_end - u0 - warp + kWarps - 1) / kWarps : 0);
         st.clear();
-        if (cur.x >= 0 && (unit_t)cur.x < x_end) {
+        if (cur.x >= 0) {
             load_queries<NT>(a.q + row0 * kHeadDim, G, a.scale_log2, qb, mul);
-            run(x_end, __ldg(a.q_pos + t));
+            run(n_all, __ldg(a.q_pos + t));
         }
         st.sum_lanes();
         const int g = lane >> 2, cq = lane & 3;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int h0 = 8 * nt + 2 * cq;
-            float *r0 = s_mo + (warp * P::kRows + h0) * kMergeStride, *r1 = r0 + kMergeStride;
+            float *r0 = reinterpret_cast<float *>(gbase + warp * kRingBytes) + h0 * kMergeStride, *r1 = r0 + kMergeStride;
 #pragma unroll
             for (int dm = 0; dm < 8; ++dm) {
-                const int d = 16 * dm + 2 * g;
-                *reinterpret_cast<float2 *>(r0 + d) = make_float2(st.o[dm][nt][0], st.o[dm][nt][2]);
-                *reinterpret_cast<float2 *>(r1 + d) = make_float2(st.o[dm][nt][1], st.o[dm][nt][3]);
+                const int d = 16 * dm + g;
+                r0[d] = st.o[dm][nt][0];
+                r1[d] = st.o[dm][nt][1];
+                r0[d + 8] = st.o[dm][nt][2];
+                r1[d + 8] = st.o[dm][nt][3];
             }
             if (g == 0) {
-                float *ml = s_ml + (warp * P::kRows + h0) * 2;
+                float *ml = s_ml + (warp * 16 + h0) * 2;
                 ml[0] = st.m[nt][0]; ml[1] = st.l[nt][0];
                 ml[2] = st.m[nt][1]; ml[3] = st.l[nt][1];
             }
         }
-        __syncthreads();
-        const bool whole = u == tail_pair * K && seg_end == (tail_pair + 1) * K;
-        for (int e = tid; e < G * 32; e += kThreads) {
+        const int w0 = warp - member, bar = 1 + warp / team;   // a named barrier per team
+        named_barrier(bar, team * 32);
+        for (int e = member * 32 + lane; e < G * 32; e += team * 32) {
             const int r = e >> 5, d0 = (e & 31) * 4;
+            const float *ml = s_ml + (w0 * 16 + r) * 2;
+            const float *mo = reinterpret_cast<const float *>(gbase + w0 * kRingBytes) + r * kMergeStride + d0;
             float M = -INFINITY, L = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[(w * P::kRows + r) * 2]);
+            for (int w = 0; w < team; ++w) M = fmaxf(M, ml[w * 32]);
             if (M != -INFINITY)
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float m = s_ml[(w * P::kRows + r) * 2];
+                for (int w = 0; w < team; ++w) {
+                    const float m = ml[w * 32];
                     if (m == -INFINITY) continue;
                     const float f = exp2f(m - M);
-                    L += s_ml[(w * P::kRows + r) * 2 + 1] * f;
-                    const float4 v = *reinterpret_cast<const float4 *>(s_mo + (w * P::kRows + r) * kMergeStride + d0);
+                    L += ml[w * 32 + 1] * f;
+                    const float4 v = *reinterpret_cast<const float4 *>(mo + w * (kRingBytes / 4));
                     acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
                 }
-            if (whole) {
+            if (splits == 1) {
                 const float inv = inv_of(L);
                 *reinterpret_cast<uint2 *>(a.out + (row0 + r) * kHeadDim + d0) =
                     make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
                 if (a.lse && d0 == 0) a.lse[row0 + r] = lse_of(M, L);
             } else {
-                // a CTA's range cuts at most two pairs: its first and its last
-                float *dst = a.part + ((size_t)(2 * c + (u == u0 ? 0 : 1)) * G + r) * kAttnPartStride;
+                float *dst = a.part + ((size_t)c * G + r) * kAttnPartStride;
                 *reinterpret_cast<float4 *>(dst + d0) = acc;
                 if (d0 == 0) *reinterpret_cast<float2 *>(dst + 128) = make_float2(M, L);
             }
         }
-        __syncthreads();   // the merge rows are free; the partial's stores are ordered before the count
-        if (!whole) {
-            if (tid == 0) {
-                const int covered = (int)(seg_end - u);
-                *s_last = atomic_add_acq_rel_gpu(a.counters + pair, covered) + covered == (int)K;
-            }
+        if (splits > 1) {   // the team is the CTA
+            __syncthreads();   // the partial's stores are ordered before the count
+            if (tid == 0) *s_last = atomic_add_acq_rel_gpu(a.counters + tail_pair, 1) + 1 == splits;
             __syncthreads();
             if (*s_last) {
-                // the pair's CTAs are this CTA's neighbours (ranges are contiguous)
-                const unit_t p_lo = tail_pair * K, p_hi = p_lo + K;
-                int cf = c, cl = c;
-                while (cf > 0 && s_rb[cf] > p_lo) --cf;
-                while (cl + 1 < a.num_ctas && s_rb[cl + 1] < p_hi) ++cl;
-                const int n = min(cl - cf + 1, kMaxSplitSlots);
-                for (int e = tid; e < G * 32; e += kThreads) {
+                const int c0 = c / splits * splits;
+                for (int e = tid; e < G * 32; e += threads) {
                     const int r = e >> 5, d0 = (e & 31) * 4;
                     float M = -INFINITY, L = 0.f;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     constexpr int kBatch = 4;   // partials in flight per round trip
-                    for (int k0 = 0; k0 < n; k0 += kBatch) {
+                    for (int k0 = 0; k0 < splits; k0 += kBatch) {
                         float2 ml[kBatch];
                         float4 ov[kBatch];
 #pragma unroll
                         for (int k = 0; k < kBatch; ++k) {
-                            const int cc = cf + k0 + k;
                             ml[k] = make_float2(-INFINITY, 0.f);
                             ov[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (k0 + k < n) {
-                                const int slot = 2 * cc + (s_rb[cc] >= p_lo ? 0 : 1);
-                                const float *src = a.part + ((size_t)slot * G + r) * kAttnPartStride;
+                            if (k0 + k < splits) {
+                                const float *src = a.part + ((size_t)(c0 + k0 + k) * G + r) * kAttnPartStride;
                                 ml[k] = __ldcg(reinterpret_cast<const float2 *>(src + 128));
                                 ov[k] = __ldcg(reinterpret_cast<const float4 *>(src + d0));
                             }
@@ -664,10 +670,9 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
                     if (a.lse && d0 == 0) a.lse[row0 + r] = lse_of(M, L);
                 }
-                if (tid == 0) a.counters[pair] = 0;
+                if (tid == 0) a.counters[tail_pair] = 0;
             }
         }
-        u = seg_end;
     }
     err_bits = __reduce_or_sync(0xffffffffu, err_bits);
     if (lane == 0 && err_bits) set_err(a.dev_err, err_bits);
@@ -676,7 +681,13 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         // limit) before the CTA's shared memory goes to the next one
         if (lane == 0) {
             set_err(a.dev_err, DSA_DEV_ERR_WAIT);
-            for (; taken < issued; ++taken) mbar_wait(bars + 8 * (taken % kSlots), (taken / kSlots) & 1, s_never);
+            for (; in_flight > 0; --in_flight) {
+                mbar_wait(bars + 8 * slot, phase, s_never);
+                if (++slot == kSlots) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
         }
         __syncwarp();
     }
@@ -717,7 +728,7 @@ cudaError_t pool_map(CUtensorMap &m, const void *pool, const AttnArgs &a) {
 }
 
 template <int NT>
-cudaError_t launch(const AttnArgs &a, const CUtensorMap &k, const CUtensorMap &v, int ctas, cudaStream_t stream) {
+cudaError_t launch(const AttnArgs &a, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t stream) {
     // the shared-memory opt-in, once per device
     static std::atomic<unsigned long long> done{0};
     int dev = 0;
@@ -725,21 +736,21 @@ cudaError_t launch(const AttnArgs &a, const CUtensorMap &k, const CUtensorMap &v
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(done.load() >> dev & 1)) {
         e = cudaFuncSetAttribute(sparse_attn_fp8_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Plan<NT>::kSmemBytes);
+                                 Plan(fp8_max_warps(NT)).bytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) done.fetch_or(1ull << dev);
     }
-    return launch_pdl(sparse_attn_fp8_kernel<NT>, dim3(ctas), dim3(kThreads), Plan<NT>::kSmemBytes, stream, k, v, a);
+    return launch_pdl(sparse_attn_fp8_kernel<NT>, dim3(a.num_ctas), dim3(a.warps * 32), (size_t)Plan(a.warps).bytes, stream, k, v, a);
 }
 
 }  // namespace
 
-cudaError_t launch_sparse_attn_fp8(const AttnArgs &a, int ctas, cudaStream_t stream) {
+cudaError_t launch_sparse_attn_fp8(const AttnArgs &a, cudaStream_t stream) {
     CUtensorMap k, v;
     cudaError_t e = pool_map(k, a.k_pool, a);
     if (e == cudaSuccess) e = pool_map(v, a.v_pool, a);
     if (e != cudaSuccess) return e;
-    return a.group <= 8 ? launch<1>(a, k, v, ctas, stream) : launch<2>(a, k, v, ctas, stream);
+    return a.group <= 8 ? launch<1>(a, k, v, stream) : launch<2>(a, k, v, stream);
 }
 
 }  // namespace dsa

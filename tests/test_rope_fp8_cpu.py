@@ -178,15 +178,31 @@ def test_binding_refuses_mismatched_shapes():
         kw = dict(k_pool=c8.k_pool, v_pool=c8.v_pool, kc_pool=c8.kc_pool, k_scale=c8.k_scale, v_scale=c8.v_scale)
         kw.update(bad)
         with pytest.raises(ValueError):
-            dsa.PagedKVCacheFP8(**kw).ctype()
+            dsa.PagedKVCacheFP8(**kw).packed(-1)
     with pytest.raises(ValueError, match="pair_axis"):
-        dsa.Rotary(torch.ones(64), num_axes=3).ctype()
+        dsa.Rotary(torch.ones(64), num_axes=3).packed(-1)
     with pytest.raises(ValueError, match="pair_axis"):
-        dsa.Rotary(torch.ones(64), num_axes=2, pair_axis=torch.zeros(32, dtype=torch.int32)).ctype()
+        dsa.Rotary(torch.ones(64), num_axes=2, pair_axis=torch.zeros(32, dtype=torch.int32)).packed(-1)
     with pytest.raises(ValueError, match="float32"):
-        dsa.Rotary(torch.ones(64, dtype=torch.float64)).ctype()
-    sel, cnt = torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
-    for args in ((row[:, :, :64], sel, cnt), (row, sel[0], cnt), (row, sel, torch.ones(2, dtype=torch.int32)),
-                 (row.float(), sel, cnt), (row, sel.long(), cnt)):
-        with pytest.raises(ValueError):
-            dsa.sparse_attn_prefill_fp8(c8, s, q, *args)
+        dsa.Rotary(torch.ones(64, dtype=torch.float64)).packed(-1)
+    with pytest.raises(ValueError, match="seq_lens"):
+        dsa.SeqBatch(s.block_table, torch.ones(2, dtype=torch.int32)).packed(-1)
+    with pytest.raises(ValueError, match="contiguous"):
+        dsa.SeqBatch(torch.zeros(2, 4, dtype=torch.int32)[:, ::2], torch.ones(2, dtype=torch.int32)).packed(-1)
+    with pytest.raises(ValueError, match="other tensors"):
+        dsa._at(row, torch.bfloat16, 0, "row") if row.get_device() >= 0 else dsa._wrong_device(1, 0, "row")
+
+
+def test_packed_structs_have_the_c_layout():
+    """The packed bytes are the ctypes structures' bytes (up to the padding at their end)."""
+    def same(packed, c):
+        raw = bytes(c)
+        assert raw[:len(packed)] == packed and len(raw) - len(packed) < 8
+
+    same(_lib.pack_cache(1, 2, 3, 4, 5, 6, 7, 8), _lib.KvCacheC(1, 2, 3, 4, 5, 6, 7, 8))
+    same(_lib.pack_cache_fp8(1, 2, 3, 4, 5, 6, 7, 8, 9, 10), _lib.KvCacheFp8C(1, 2, 3, 4, 5, 6, 7, 8, 9, 10))
+    same(_lib.pack_seqs(1, 2, 3, 4), _lib.SeqsC(1, 2, 3, 4))
+    same(_lib.pack_queries(1, 2, 3), _lib.QueriesC(1, 2, 3))
+    same(_lib.pack_rope(1, 2, 3, 4, 5, 0.5), _lib.RopeC(1, 2, 3, 4, 5, 0.5))
+    same(_lib.pack_new_tokens(1, 2, 3, 4, 5, 6, 7, 8), _lib.NewTokensC(1, 2, 3, 4, 5, 6, 7, 8))
+    same(_lib.pack_query_rows(1, 2, 3, 4, 5), _lib.QueryRowsC(1, 2, 3, 4, 5))
