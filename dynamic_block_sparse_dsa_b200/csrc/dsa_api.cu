@@ -732,13 +732,15 @@ int dsa_kv_append_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *seqs, const
     if (rc) return rc;
     a.k_scale = cache->k_scale;
     a.v_scale = cache->v_scale;
-    // a CTA of a decode batch takes all heads of its tile (one new row each); a
-    // full tile is 64 rows per head already
-    const bool few = a.kv.total_new <= 4ll * a.kv.num_seqs;
-    a.heads_per_cta = few ? a.kv.num_kv_heads : 1;
-    const long long tiles = append_fp8_tile_ctas(a.kv.total_new, a.kv.num_seqs, a.kv.num_kv_heads, a.heads_per_cta);
-    if (tiles + a.total_q >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
-    a.tile_ctas = (int)tiles;
+    // heads that share a tile's rotation tables, one after the other: with 4 (2)
+    // instead of 8, 64 decode tokens and two 2048-token chunks of 8 heads took 32.4
+    // (37.4) us instead of 30.4
+    a.heads_per_item = 8;
+    const long long units = a.kv.total_new > 0 ? a.kv.total_new / kBlockSize + 2ll * a.kv.num_seqs : 0;
+    const long long groups = (a.kv.num_kv_heads + a.heads_per_item - 1) / a.heads_per_item;
+    const long long items = units * 2 * groups;
+    if (items + a.total_q >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
+    a.tile_ctas = (int)items;
     return from_cuda(launch_kv_append_fp8(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

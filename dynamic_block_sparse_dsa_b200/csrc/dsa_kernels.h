@@ -66,8 +66,8 @@ struct AppendRopeArgs {
     __nv_bfloat16 *q_out;           // [total_q][num_q_heads][128]
     // E4M3 cache only
     float *k_scale, *v_scale;       // [num_pages][block_size / 64][num_kv_heads]
-    int heads_per_cta;              // KV heads per append CTA
-    int tile_ctas;                  // append CTAs (the query CTAs come after them)
+    int heads_per_item;             // KV heads per append item
+    int tile_ctas;                  // CTAs for the append's items (the query CTAs come after)
 };
 
 struct IndexScoreArgs {
@@ -217,8 +217,6 @@ struct FusedArgs {
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t stream);
 cudaError_t launch_kv_append_rope(const AppendRopeArgs &a, cudaStream_t stream);
 cudaError_t launch_kv_append_fp8(const AppendRopeArgs &a, cudaStream_t stream);
-// append CTAs of launch_kv_append_fp8 (the host checks that the grid is in range)
-long long append_fp8_tile_ctas(int total_new, int num_seqs, int num_kv_heads, int heads_per_cta);
 cudaError_t launch_index_score(const IndexScoreArgs &a, cudaStream_t stream);
 // tensor-core (tcgen05 int8) scoring for batches with many queries per sequence
 cudaError_t launch_index_score_tc(const IndexScoreArgs &a, int num_sms, cudaStream_t stream);

@@ -11,8 +11,10 @@
 // At a million tokens p * inv_freq in fp32 is off by up to 0.06 rad, so the
 // angle is kept in turns as a 64-bit fraction: f = inv_freq / (2 pi) mod 1
 // times 2^64, and p * f mod 2^64 is the fraction of a turn, exact but for the
-// rounding of f (2^-53 of a turn per position).  Its upper 32 bits go through
-// sincospif.  The rotation itself is fp32, rounded once to the stored type.
+// rounding of f (2^-53 of a turn per position).  Its upper 32 bits give the
+// octant pair and a remainder in [-pi/4, pi/4], whose sine and cosine are Taylor
+// sums (to x^9 and x^8: the next terms are below 2^-25 there).  The rotation
+// itself is fp32, rounded once to the stored type.
 //
 // E4M3 cache.  A tile is 64 tokens of a block; each (tile, KV head) has one
 // scale for K and one for V, a power of two when written here:
@@ -31,10 +33,11 @@ namespace dsa {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kSlots = kThreads / 8;   // rows in flight per pass: eight threads (32 bytes each) per row
+constexpr int kThreads = 256, kSlots = kThreads / 8;   // eight threads (32 bytes of a row each) per row
+constexpr int kTileThreads = 2 * kThreads;             // E4M3 append: a row of a full tile per eight threads
 constexpr int kPairs = kHeadDim / 2;
 constexpr int kMinScaleExp = -100;
+constexpr int kMaxAxes = 4;
 
 // the fraction of a turn per position as a 64-bit fixed-point number
 __device__ __forceinline__ unsigned long long turns_q64(float inv_freq) {
@@ -45,10 +48,17 @@ __device__ __forceinline__ unsigned long long turns_q64(float inv_freq) {
 
 // (cos, sin) of the angle at position p, times the rotation's scale
 __device__ __forceinline__ float2 rope_cs(int p, unsigned long long f, float scale) {
-    const int hi = (int)(((unsigned long long)(long long)p * f) >> 32);
-    float s, c;
-    sincospif((float)hi * 0x1p-31f, &s, &c);
-    return make_float2(c * scale, s * scale);
+    const uint32_t turn = (uint32_t)(((unsigned long long)(long long)p * f) >> 32);   // of 2^32
+    const uint32_t quarter = (turn + 0x20000000u) >> 30;                               // nearest quarter turn
+    const float x = (float)(int)(turn - (quarter << 30)) * (float)(3.14159265358979323846 / 2147483648.0);
+    const float y = x * x;
+    float s = fmaf(y, fmaf(y, fmaf(y, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f);
+    s = fmaf(x * y, s, x);
+    const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, 1.f / 40320.f, -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+    // a quarter turn on: (c, s) -> (-s, c)
+    const float u = (quarter & 1u) ? s : c, v = (quarter & 1u) ? c : s;
+    const float cs = ((quarter + 1u) & 2u) ? -u : u, sn = (quarter & 2u) ? -v : v;
+    return make_float2(cs * scale, sn * scale);
 }
 
 // the (cos, sin) table of one row: thread j of the row owns pairs 8j..8j+7,
@@ -126,16 +136,12 @@ __device__ __forceinline__ int last_le_warp(int n, int i, F value) {
     return lo;
 }
 
-// position of row i on the axis of `pair`
-__device__ __forceinline__ int axis_pos(const RopeArgs &r, const int32_t *pos, int total, int i, int pair,
-                                        int plain, uint32_t &err) {
-    if (!pos) return plain;
-    int axis = r.pair_axis ? __ldg(r.pair_axis + pair) : 0;
-    if (axis < 0 || axis >= r.num_axes) {
-        err |= DSA_DEV_ERR_POS;
-        axis = 0;
-    }
-    return __ldg(pos + (size_t)axis * total + i);
+// the axis that `pair` turns by
+__device__ __forceinline__ int axis_of(const RopeArgs &r, int pair, uint32_t &err) {
+    const int axis = r.pair_axis ? __ldg(r.pair_axis + pair) : 0;
+    if (axis >= 0 && axis < r.num_axes) return axis;
+    err |= DSA_DEV_ERR_POS;
+    return 0;
 }
 
 // where a new token lands; page < 0 when it is skipped
@@ -171,12 +177,12 @@ __device__ __forceinline__ Place place_of(const KvAppendArgs &a, int i, uint32_t
 // the rotated query rows of one query and, in the bf16 cache, the K and V rows
 // of one new token: row r of the CTA's list is K head r, then V head, then
 // query head.  Loads of kBatch rows per thread are issued before the tables
-// are ready and before the wait for the kernels ahead.
+// (s_tab: K, q) are ready and before the wait for the kernels ahead.  kThreads
+// threads numbered tid share it; all threads of the CTA call it.
 template <bool kKv>
-__device__ __forceinline__ void token_rows(const AppendRopeArgs &a, int i) {
-    __shared__ RopeTab s_tab[2];   // K, q
-    constexpr int kBatch = 3;
-    const int tid = threadIdx.x, j = tid & 7, slot = tid >> 3;
+__device__ __forceinline__ void token_rows(const AppendRopeArgs &a, int i, int tid, RopeTab *s_tab) {
+    constexpr int kBatch = 2;
+    const int j = tid & 7, slot = tid >> 3;
     const bool has_new = kKv && i < a.kv.total_new, has_q = i < a.total_q;
     const int hkv = has_new ? a.kv.num_kv_heads : 0, nq = has_q ? a.num_q_heads : 0;
     const int rows = 2 * hkv + nq;
@@ -207,8 +213,10 @@ __device__ __forceinline__ void token_rows(const AppendRopeArgs &a, int i) {
         const int pair = tid & (kPairs - 1);
         const bool is_q = tid >= kPairs;
         if (pair < (r.rotary_dim >> 1) && (is_q ? has_q : has_new)) {
-            const int pos = is_q ? axis_pos(r, a.pos_q, a.total_q, i, pair, a.pos_q ? 0 : __ldg(a.q_pos + i), err)
-                                 : axis_pos(r, a.pos_new, a.kv.total_new, i, pair, p.pos, err);
+            const int axis = axis_of(r, pair, err);
+            int pos = p.pos;
+            if (is_q) pos = a.pos_q ? __ldg(a.pos_q + (size_t)axis * a.total_q + i) : __ldg(a.q_pos + i);
+            else if (a.pos_new) pos = __ldg(a.pos_new + (size_t)axis * a.kv.total_new + i);
             put_cs(s_tab[is_q], pair, rope_cs(pos, turns_q64(__ldg(r.inv_freq + pair)), r.scale));
         }
     }
@@ -281,184 +289,223 @@ __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float ratio) {
     return a | (b << 16);
 }
 
-constexpr int kRowsPT = 2;                    // rows whose values a thread holds while the maximum forms
-constexpr int kPassRows = kRowsPT * kSlots;   // = 64: a full tile of one head
+constexpr int kPassRows = kTileThreads / 8;
+static_assert(kPassRows == kBlockSize, "a pass holds a full tile of one head");
 
-// One CTA per (tile with new tokens, K or V, group of heads).  A pass takes as
-// many heads as fit 64 rows -- one head of a full tile, all heads of a decode
-// token -- and holds their values in registers between the maximum and the
-// stores, so the new rows are read once.
-__device__ __forceinline__ void tile_rows(const AppendRopeArgs &a, int item) {
-    __shared__ RopeTab s_tab[kBlockSize];
-    __shared__ unsigned long long s_freq[kPairs];
+// an append item: the new rows of one tile, K or V, for the heads [h_begin, h_end)
+struct Item {
+    int page, t0, len;      // t0: the tile's first position
+    int held, cnt, i0;      // slots filled before, new tokens (0: nothing to do), the first of them
+    int h_begin, h_end;
+    bool is_v;
+};
+
+// Item number `item` = ((unit * 2) + is_v) * groups + head group, by one warp.
+// Sequence s owns the units from cu_new[s] / 64 + 2 s on: n tokens lie in at
+// most n / 64 + 2 tiles, and the next sequence starts no earlier.  Units behind a
+// sequence's tiles have nothing to do.  (Counting the tiles exactly, 32
+// sequences at a time, left fewer idle CTAs but took 2 us longer to find one's
+// work: 32 decode tokens 5.0 against 2.8 us.)
+__device__ __forceinline__ Item find_item(const AppendRopeArgs &a, int item) {
+    const KvAppendArgs &kv = a.kv;
+    const int H = kv.num_kv_heads, groups = (H + a.heads_per_item - 1) / a.heads_per_item;
+    Item it{};
+    const int g = item % groups;
+    it.h_begin = g * a.heads_per_item;
+    it.is_v = (item / groups) & 1;
+    const int unit = item / (2 * groups);
+    const bool reports = (threadIdx.x & 31) == 0 && g == 0 && !it.is_v;
+    const int s = last_le_warp(kv.num_seqs, unit, [&](int k) { return (__ldg(kv.cu_new + k) >> 6) + 2 * k; });
+    const int first = __ldg(kv.cu_new + s), last = __ldg(kv.cu_new + s + 1);
+    it.len = __ldg(kv.seq_lens + s);
+    if (unit == 0 && reports && __ldg(kv.cu_new + kv.num_seqs) < kv.total_new) set_err(kv.dev_err, DSA_DEV_ERR_POS);
+    const int n = last - first;
+    if (first < 0 || n < 0 || last > kv.total_new || n > it.len) {
+        if (reports) set_err(kv.dev_err, DSA_DEV_ERR_POS);
+        return it;
+    }
+    const int pos0 = it.len - n;                                 // first new position
+    const long long t0 = ((long long)(pos0 >> 6) + unit - ((first >> 6) + 2 * s)) << 6;
+    if (n == 0 || t0 >= it.len) return it;
+    it.t0 = (int)t0;
+    it.held = max(pos0 - it.t0, 0);
+    const int cnt = min(it.len - it.t0, kBlockSize) - it.held;   // 1..64
+    // where one pass holds every head, the first group takes them all
+    const bool one_pass = cnt * H <= kPassRows;
+    if (one_pass && g > 0) return it;
+    const int blk = it.t0 >> kv.block_shift;
+    if (blk >= kv.max_blocks) {
+        if (reports) set_err(kv.dev_err, DSA_DEV_ERR_POS);
+        return it;
+    }
+    it.page = __ldg(kv.block_table + (size_t)s * kv.max_blocks + blk);
+    if (it.page < 0 || it.page >= kv.num_pages) {
+        if (reports) set_err(kv.dev_err, DSA_DEV_ERR_PAGE);
+        return it;
+    }
+    it.i0 = first + (it.t0 + it.held - pos0);
+    it.h_end = one_pass ? H : min(it.h_begin + a.heads_per_item, H);
+    it.cnt = cnt;
+    return it;
+}
+
+// One item by the CTA.  A pass takes as many heads as fit 64 rows -- one head of
+// a full tile, all heads of a decode token -- and holds their values in
+// registers between the maximum and the stores, so the new rows are read once.
+__device__ __forceinline__ void tile_rows(const AppendRopeArgs &a, int item, RopeTab *s_tab) {
+    __shared__ int s_pos[kMaxAxes][kBlockSize];
     __shared__ uint32_t s_amax[kPassRows];
     __shared__ float s_old[kPassRows], s_new[kPassRows];
+    __shared__ Item s_item;
     const KvAppendArgs &kv = a.kv;
     const RopeArgs &r = a.rope;
     const int tid = threadIdx.x, j = tid & 7, slot = tid >> 3;
-    const int groups = (kv.num_kv_heads + a.heads_per_cta - 1) / a.heads_per_cta;
-    const bool is_v = (item / groups) & 1;
-    const int h_begin = (item % groups) * a.heads_per_cta;
-    const int h_end = min(h_begin + a.heads_per_cta, kv.num_kv_heads);
-    const int unit = item / (2 * groups);
-    // sequence s owns the units from cu_new[s] / 64 + 2 s on: n tokens lie in
-    // at most n / 64 + 2 tiles, and the next sequence starts no earlier
-    const int s = last_le_warp(kv.num_seqs, unit, [&](int k) { return (__ldg(kv.cu_new + k) >> 6) + 2 * k; });
-    const int first = __ldg(kv.cu_new + s), last = __ldg(kv.cu_new + s + 1), len = __ldg(kv.seq_lens + s);
-    const bool reports = tid == 0 && h_begin == 0 && !is_v;
-    if (unit == 0 && reports && __ldg(kv.cu_new + kv.num_seqs) < kv.total_new) set_err(kv.dev_err, DSA_DEV_ERR_POS);
-    const int n = last - first;
-    if (first < 0 || n < 0 || last > kv.total_new || n > len) {
-        if (reports) set_err(kv.dev_err, DSA_DEV_ERR_POS);
-        return;
+    if (tid < 32) {   // one warp: copies of this chain in every warp would cost more than the rows
+        const Item it = find_item(a, item);
+        if (tid == 0) s_item = it;
     }
-    const int pos0 = len - n;                                    // first new position
-    const long long t0_wide = ((long long)(pos0 >> 6) + unit - ((first >> 6) + 2 * s)) << 6;
-    if (n == 0 || t0_wide >= len) return;
-    const int t0 = (int)t0_wide;                                 // this tile's first position
-    const int blk = t0 >> kv.block_shift;
-    if (blk >= kv.max_blocks) {
-        if (reports) set_err(kv.dev_err, DSA_DEV_ERR_POS);
-        return;
-    }
-    const int page = __ldg(kv.block_table + (size_t)s * kv.max_blocks + blk);
-    if (page < 0 || page >= kv.num_pages) {
-        if (reports) set_err(kv.dev_err, DSA_DEV_ERR_PAGE);
-        return;
-    }
-    const int held = max(pos0 - t0, 0);                          // slots filled before
-    const int cnt = min(len - t0, kBlockSize) - held;            // new tokens of the tile, 1..64
-    const int i0 = first + (t0 + held - pos0);                   // the first of them
-    const int H = kv.num_kv_heads;
-    const size_t row0 = ((size_t)page << kv.block_shift) + (t0 & ((1 << kv.block_shift) - 1));   // pool row of slot 0
-    uint8_t *pool = static_cast<uint8_t *>(is_v ? kv.v_pool : kv.k_pool) + row0 * H * kHeadDim;
-    float *scales = (is_v ? a.v_scale : a.k_scale) + (row0 >> 6) * H;
-    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(is_v ? kv.v_new : kv.k_new);
-    const long long stride = is_v ? a.v_stride : a.k_stride;
-    const bool rotated = !is_v && r.rotary_dim > 0;
+    __syncthreads();
+    const Item it = s_item;
+    const int cnt = it.cnt, held = it.held, H = kv.num_kv_heads;
+    if (cnt == 0) return;
+    const int per_pass = min(kPassRows / cnt, it.h_end - it.h_begin);   // heads per pass
+    const size_t row0 = ((size_t)it.page << kv.block_shift) + (it.t0 & ((1 << kv.block_shift) - 1));   // pool row of slot 0
+    uint8_t *pool = static_cast<uint8_t *>(it.is_v ? kv.v_pool : kv.k_pool) + row0 * H * kHeadDim;
+    float *scales = (it.is_v ? a.v_scale : a.k_scale) + (row0 >> 6) * H;
+    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(it.is_v ? kv.v_new : kv.k_new);
+    const long long stride = it.is_v ? a.v_stride : a.k_stride;
+    const bool rotated = !it.is_v && r.rotary_dim > 0;
     const bool turned = rotated && j < (r.rotary_dim >> 4);
     int c0 = 2 * j, c1 = 2 * j + 1;
     if (rotated) own_chunks(r, j, c0, c1);
 
+    // row `slot` of a pass is (head, token); a pass of one head needs no division
+    const int rh = per_pass == 1 ? (slot < cnt ? 0 : kPassRows) : slot / cnt;
+    const int rt = per_pass == 1 ? slot : slot - rh * cnt;
+    const __nv_bfloat16 *mine = src + (it.i0 + rt) * stride + rh * kHeadDim;
+    uint4 raw0, raw1;
+    auto fetch = [&](int hb, int nh) {
+        if (rh < nh) {
+            raw0 = reinterpret_cast<const uint4 *>(mine + hb * kHeadDim)[c0];
+            raw1 = reinterpret_cast<const uint4 *>(mine + hb * kHeadDim)[c1];
+        }
+    };
+    fetch(it.h_begin, per_pass);   // on their way while the tables form
     uint32_t err = 0;
     if (rotated) {
-        if (tid < (r.rotary_dim >> 1)) s_freq[tid] = turns_q64(__ldg(r.inv_freq + tid));
+        for (int e = tid; e < r.num_axes * cnt; e += kTileThreads) {
+            const int axis = e / cnt, tok = e - axis * cnt;
+            s_pos[axis][tok] = a.pos_new ? __ldg(a.pos_new + (size_t)axis * kv.total_new + it.i0 + tok)
+                                         : it.t0 + held + tok;
+        }
         __syncthreads();
-        for (int e = tid; e < cnt * kPairs; e += kThreads) {
-            const int tok = e / kPairs, pair = e % kPairs;
-            if (pair < (r.rotary_dim >> 1)) {
-                const int pos = axis_pos(r, a.pos_new, kv.total_new, i0 + tok, pair, t0 + held + tok, err);
-                put_cs(s_tab[tok], pair, rope_cs(pos, s_freq[pair], r.scale));
-            }
+        const int pair = tid % kPairs;   // the same pair for all of the thread's entries
+        if (pair < (r.rotary_dim >> 1)) {
+            const int axis = axis_of(r, pair, err);
+            const unsigned long long f = turns_q64(__ldg(r.inv_freq + pair));
+            for (int tok = tid / kPairs; tok < cnt; tok += kTileThreads / kPairs)
+                put_cs(s_tab[tok], pair, rope_cs(s_pos[axis][tok], f, r.scale));
         }
     }
-    const int per_pass = min(kPassRows / cnt, h_end - h_begin);   // heads per pass (cnt <= 64)
-    bool waited = false;
-    for (int hb = h_begin; hb < h_end; hb += per_pass) {
-        const int nh = min(per_pass, h_end - hb);
-        float x[kRowsPT][16];
-        if (tid < nh) s_amax[tid] = 0u;
-#pragma unroll
-        for (int k = 0; k < kRowsPT; ++k) {
-            const int row = k * kSlots + slot;
-            if (row < nh * cnt) {
-                const int h = row / cnt, tok = row - h * cnt;
-                const uint4 *p = reinterpret_cast<const uint4 *>(src + (i0 + tok) * stride + (size_t)(hb + h) * kHeadDim);
-                unpack8(p[c0], x[k]);
-                unpack8(p[c1], x[k] + 8);
-            }
+    // the scales and codes held from before, and every store, come after the kernels ahead
+    pdl_wait();
+    for (int hb = it.h_begin; hb < it.h_end; hb += per_pass) {
+        const int nh = min(per_pass, it.h_end - hb);
+        if (tid < nh) {
+            s_amax[tid] = 0u;
+            if (held > 0) s_old[tid] = ld_ordered_cg(scales + hb + tid);
         }
-        if (!waited) {   // the scales and codes held from before, and every store, come after the kernels ahead
-            pdl_wait();
-            waited = true;
-        }
-        if (tid < nh && held > 0) s_old[tid] = ld_ordered_cg(scales + hb + tid);
-        __syncthreads();   // tables, cleared maxima, held scales
+        float x[16];
+        unpack8(raw0, x);
+        unpack8(raw1, x + 8);
+        if (hb + per_pass < it.h_end) fetch(hb + per_pass, min(per_pass, it.h_end - hb - per_pass));   // the next pass's rows
+        __syncthreads();     // tables, cleared maxima, held scales
+        uint32_t top = 0u;   // magnitudes order as their bits, infinities and NaN above them
+        if (rh < nh) {
+            if (turned) rotate16(x, s_tab[rt], j, r.interleaved);
 #pragma unroll
-        for (int k = 0; k < kRowsPT; ++k) {
-            const int row = k * kSlots + slot;
-            float m = 0.f;
-            if (row < nh * cnt) {
-                const int tok = row - (row / cnt) * cnt;
-                if (turned) rotate16(x[k], s_tab[tok], j, r.interleaved);
+            for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+            if (top >= 0x7f800000u) {   // some are not finite: the largest of the others
+                err |= DSA_DEV_ERR_VALUE;
+                top = 0u;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float v = fabsf(x[k][e]);
-                    if (v <= FLT_MAX) m = fmaxf(m, v);
-                    else err |= DSA_DEV_ERR_VALUE;
+                    const uint32_t v = __float_as_uint(x[e]) & 0x7fffffffu;
+                    if (v < 0x7f800000u) top = max(top, v);
                 }
             }
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-            // the maximum does not depend on the order (non-negative floats order as their bits)
-            if (j == 0 && row < nh * cnt) atomicMax(&s_amax[row / cnt], __float_as_uint(m));
         }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        // the maximum does not depend on the order
+        if (j == 0 && rh < nh) atomicMax(&s_amax[rh], top);
         __syncthreads();
+        bool grows = false;
         if (tid < nh) {
             const float need = scale_for(__uint_as_float(s_amax[tid]));
-            float now = need;
-            if (held > 0) {
-                const float was = s_old[tid];
-                // a held scale that is not a positive finite number says nothing about its codes
-                const bool good = was > 0.f && was <= FLT_MAX;
-                if (good) now = fmaxf(was, need);
-                else s_old[tid] = now;   // no rescaling
-                if (now != was) scales[hb + tid] = now;
-            } else {
-                scales[hb + tid] = now;
-            }
+            const float was = held > 0 ? s_old[tid] : 0.f;
+            // a held scale that is not a positive finite number says nothing about its codes
+            const bool good = was > 0.f && was <= FLT_MAX;
+            const float now = good ? fmaxf(was, need) : need;
+            if (now != was) scales[hb + tid] = now;
+            grows = good && now != was;
+            if (!grows) s_old[tid] = now;   // no rescaling
             s_new[tid] = now;
         }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kRowsPT; ++k) {
-            const int row = k * kSlots + slot;
-            if (row < nh * cnt) {
-                const int h = row / cnt, tok = row - h * cnt;
-                const float inv = 1.f / s_new[h];
-                uint2 *dst = reinterpret_cast<uint2 *>(pool + ((size_t)(held + tok) * H + hb + h) * kHeadDim);
-                dst[c0] = to_e4m3x8(x[k], inv);
-                dst[c1] = to_e4m3x8(x[k] + 8, inv);
-            }
+        const bool grown = __syncthreads_or(grows);
+        if (rh < nh) {
+            const float inv = 1.f / s_new[rh];
+            uint2 *dst = reinterpret_cast<uint2 *>(pool + ((size_t)(held + rt) * H + hb + rh) * kHeadDim);
+            dst[c0] = to_e4m3x8(x, inv);
+            dst[c1] = to_e4m3x8(x + 8, inv);
         }
-        if (held > 0) {
-            for (int h = 0; h < nh; ++h) {
-                if (s_old[h] == s_new[h]) continue;   // the same for the whole CTA
+        if (grown)   // held rows (head, token) over the slots
+            for (int row = slot; row < nh * held; row += kPassRows) {
+                const int h = row / held, tok = row - h * held;
+                if (s_old[h] == s_new[h]) continue;
                 const float ratio = s_old[h] / s_new[h];
-                for (int tok = slot; tok < held; tok += kSlots) {
-                    uint4 *w = reinterpret_cast<uint4 *>(pool + ((size_t)tok * H + hb + h) * kHeadDim) + j;
-                    uint4 c = *w;   // a plain load stays behind the wait
-                    c.x = rescale_e4m3x4(c.x, ratio);
-                    c.y = rescale_e4m3x4(c.y, ratio);
-                    c.z = rescale_e4m3x4(c.z, ratio);
-                    c.w = rescale_e4m3x4(c.w, ratio);
-                    *w = c;
-                }
+                uint4 *w = reinterpret_cast<uint4 *>(pool + ((size_t)tok * H + hb + h) * kHeadDim) + j;
+                uint4 c = *w;   // a plain load stays behind the wait
+                c.x = rescale_e4m3x4(c.x, ratio);
+                c.y = rescale_e4m3x4(c.y, ratio);
+                c.z = rescale_e4m3x4(c.z, ratio);
+                c.w = rescale_e4m3x4(c.w, ratio);
+                *w = c;
             }
-        }
         __syncthreads();   // the shared words of this pass are free
     }
     if (err) set_err(kv.dev_err, err);
     // the coarse key of the block that the tile's last new token ends
-    const int end = t0 + held + cnt;                             // position behind it
-    const bool ends_block = end == len || (end & ((1 << kv.block_shift) - 1)) == 0;
-    if (!is_v && h_begin == 0 && kv.kc_new && ends_block && tid < kIdxDim / 16)
-        reinterpret_cast<uint4 *>(kv.kc_pool)[(size_t)page * (kIdxDim / 16) + tid] =
-            __ldg(reinterpret_cast<const uint4 *>(kv.kc_new) + (size_t)(i0 + cnt - 1) * (kIdxDim / 16) + tid);
+    const int end = it.t0 + held + cnt;                          // position behind it
+    const bool ends_block = end == it.len || (end & ((1 << kv.block_shift) - 1)) == 0;
+    if (!it.is_v && it.h_begin == 0 && kv.kc_new && ends_block && tid < kIdxDim / 16)
+        reinterpret_cast<uint4 *>(kv.kc_pool)[(size_t)it.page * (kIdxDim / 16) + tid] =
+            __ldg(reinterpret_cast<const uint4 *>(kv.kc_new) + (size_t)(it.i0 + cnt - 1) * (kIdxDim / 16) + tid);
 }
 
 }  // namespace
 
-__global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(AppendRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) kv_append_rope_kernel(AppendRopeArgs a) {
+    __shared__ RopeTab s_tab[2];
     pdl_trigger();
-    token_rows<true>(a, blockIdx.x);
+    token_rows<true>(a, blockIdx.x, threadIdx.x, s_tab);
 }
 
-__global__ void __launch_bounds__(kThreads) kv_append_fp8_kernel(AppendRopeArgs a) {
+__global__ void __launch_bounds__(kTileThreads, 2) kv_append_fp8_kernel(AppendRopeArgs a) {
+    __shared__ RopeTab s_tab[kBlockSize];
     pdl_trigger();
-    if ((int)blockIdx.x < a.tile_ctas) tile_rows(a, blockIdx.x);
-    else token_rows<false>(a, blockIdx.x - a.tile_ctas);
+    // append and query CTAs in turn as long as there are both: the former wait on
+    // latencies (tables, maxima), the latter on memory
+    const int b = blockIdx.x, both = min(a.tile_ctas, (int)gridDim.x - a.tile_ctas);
+    const bool appends = b < 2 * both ? !(b & 1) : a.tile_ctas > both;
+    const int i = b < 2 * both ? b >> 1 : b - both;
+    if (appends) {
+        tile_rows(a, i, s_tab);
+    } else {   // a query per half of the CTA
+        const int half = threadIdx.x / kThreads;
+        token_rows<false>(a, 2 * i + half, threadIdx.x % kThreads, s_tab + 2 * half);
+    }
     // also where a CTA had nothing to do: whatever waits for this kernel waits
     // for the kernels ahead of it too
     pdl_wait();
@@ -470,16 +517,10 @@ cudaError_t launch_kv_append_rope(const AppendRopeArgs &a, cudaStream_t stream) 
     return launch_pdl(kv_append_rope_kernel, dim3(ctas), dim3(kThreads), 0, stream, a);
 }
 
-long long append_fp8_tile_ctas(int total_new, int num_seqs, int num_kv_heads, int heads_per_cta) {
-    if (total_new == 0) return 0;
-    const long long units = total_new / kBlockSize + 2ll * num_seqs;
-    return units * 2 * ((num_kv_heads + heads_per_cta - 1) / heads_per_cta);
-}
-
 cudaError_t launch_kv_append_fp8(const AppendRopeArgs &a, cudaStream_t stream) {
-    const long long ctas = (long long)a.tile_ctas + a.total_q;
+    const long long ctas = (long long)a.tile_ctas + (a.total_q + 1ll) / 2;
     if (ctas == 0) return cudaSuccess;
-    return launch_pdl(kv_append_fp8_kernel, dim3((unsigned)ctas), dim3(kThreads), 0, stream, a);
+    return launch_pdl(kv_append_fp8_kernel, dim3((unsigned)ctas), dim3(kTileThreads), 0, stream, a);
 }
 
 }  // namespace dsa
