@@ -22,6 +22,7 @@ the data path); rank 0 prints one JSON line.
 from __future__ import annotations
 
 import argparse
+import gc
 import json
 import math
 import os
@@ -858,6 +859,7 @@ def measure_workload(name, device, steps=30, iso=15, seed=None, path="auto"):
         raise RuntimeError(f"device error bits {int(err.item())} while timing {name}")
     del cases
     torch.cuda.synchronize(device)
+    gc.collect()
     torch.cuda.empty_cache()
     return rec
 
@@ -1057,6 +1059,7 @@ def main(argv=None):
         res["cpu_baseline"] = cpu_baseline(wl)
     del cases, wl
     torch.cuda.synchronize(device)
+    gc.collect()   # a StepCase and its captured steps hold each other: without this its pools stay allocated
     torch.cuda.empty_cache()
     if world == 1 and not args.no_prefill:
         res["prefill_indexer"] = prefill_indexer(device)
