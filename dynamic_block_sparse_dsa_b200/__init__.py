@@ -172,6 +172,9 @@ class PagedKVCacheFP8:
     k_scale: torch.Tensor
     v_scale: torch.Tensor
 
+    def ctype(self):
+        raise TypeError("this call works on a bf16 PagedKVCache, not on a PagedKVCacheFP8")
+
     def packed(self, dev: int) -> bytes:
         """The C description (dsa_kv_cache_fp8) of tensors on device ``dev``."""
         kp, vp, kc = self.k_pool, self.v_pool, self.kc_pool
@@ -318,6 +321,8 @@ def _append_rope(fn: str, cache, seqs: SeqBatch, cu_new, k_new, v_new, kc_new, r
     axes = 1 if rope is None else rope.num_axes
     fresh = _NOTHING_NEW
     if k_new is not None and len(k_new):
+        if v_new is None or cu_new is None:
+            raise ValueError("k_new needs v_new and cu_new")
         k, total, heads, ks = _rows(k_new, dev, "k_new")
         v, v_total, v_heads, vs = _rows(v_new, dev, "v_new")
         if heads != cache.num_kv_heads or v_heads != heads or v_total != total:
@@ -616,6 +621,8 @@ def _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, stream
         raise ValueError(f"q must be [{T}][heads][{HEAD_DIM}], got {list(q.shape)}")
     if sel.dim() != 2 or sel.shape[0] != T or cnt.numel() != T:
         raise ValueError(f"sel must be [{T}][k_max] and cnt [{T}]")
+    if queries.cu_q.numel() != seqs.seq_lens.numel() + 1:
+        raise ValueError("cu_q must have one entry more than there are sequences")
     if out is None or lse is None:
         with _on(stream):
             out, lse = _attn_out(q, out, lse)
@@ -904,7 +911,8 @@ def step(cache, seqs: SeqBatch, queries: QueryBatch, *, k_new, v_new, kc_new, q,
         return b
     if rope is not None:
         if "q_rot" not in b:
-            b["q_rot"] = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            with _on(stream):
+                b["q_rot"] = torch.empty(q.shape, dtype=q.dtype, device=dev)
         (kv_append_fp8 if fp8 else kv_append_rope)(
             cache, seqs, queries.cu_q, k_new, v_new, kc_new, rope, pos_new=pos, queries=queries, q=q, pos_q=pos,
             q_out=b["q_rot"], dev_err=dev_err, stream=stream)

@@ -472,7 +472,163 @@ def test_attention_fp8_workspace_is_reusable_and_calls_repeat(cuda_device):
         assert torch.equal(one[0], other[0]) and torch.equal(one[1], other[1])
 
 
+def test_pools_past_32_bits(cuda_device):
+    """Pools of more than 4 GiB: rows and tiles at the far end are appended to and attended over."""
+    pages, hkv = 70000, 8                       # 4.6 GB of codes each for K and V
+    pool = [torch.zeros((pages, 64, hkv, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scale = [torch.zeros((pages, 1, hkv), device="cuda") for _ in range(2)]
+    cache = dsa.PagedKVCacheFP8(*pool, torch.zeros((pages, 64), dtype=torch.int8, device="cuda"), *scale)
+    g = torch.Generator().manual_seed(41)
+    table = torch.tensor([[pages - 1, 5, pages - 2]], dtype=torch.int32, device="cuda")
+    x = torch.randn(150, hkv, 128, generator=g).bfloat16()
+    y = torch.randn(150, hkv, 128, generator=g).bfloat16()
+    seqs = dsa.SeqBatch(table, torch.tensor([150], dtype=torch.int32, device="cuda"))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dsa.kv_append_fp8(cache, seqs, torch.tensor([0, 150], dtype=torch.int32, device="cuda"), x.cuda(), y.cuda(),
+                      dev_err=err)
+    q = torch.randn(1, 8 * hkv, 128, generator=g).bfloat16()
+    queries = dsa.QueryBatch(torch.tensor([0, 1], dtype=torch.int32, device="cuda"),
+                             torch.tensor([149], dtype=torch.int32, device="cuda"))
+    sel = torch.tensor([[0, 1, 2]], dtype=torch.int32, device="cuda")
+    out, lse = dsa.sparse_attn_decode_fp8(cache, seqs, queries, q.cuda(), sel,
+                                          torch.tensor([3], dtype=torch.int32, device="cuda"), dev_err=err)
+    assert int(err) == 0
+    t = table[0].long()
+    small = [ref.stored(p[t].cpu(), s[t].cpu()) for p, s in zip(pool, scale)]
+    for got, want in zip(small, (x, y)):
+        d = (got.reshape(192, hkv, 128)[:150] - want.double()).abs()
+        step = want.double().abs() * E4M3_HALF + 2.0 ** -10 * 2.0 ** -5      # scales are at most 2^-5: |x| < 14
+        assert bool((d <= step).all())
+    w, wl, otol, ltol = ref.attention(q.double(), *small, torch.tensor([[0, 1, 2]]), 64, [0], [149], sel.cpu(), [3],
+                                      1 / math.sqrt(128))
+    assert bool(((out.cpu().double() - w).abs() <= otol).all()) and bool(((lse.cpu().double() - wl).abs() <= ltol).all())
+    assert not bool(pool[0][6].any())
+
+
 # ----------------------------------------------------------------------------- together
+
+def test_attention_right_behind_the_append(cuda_device):
+    """The attention reads the queries, codes and scales of the append launched just before it
+    (it may start early): eager and replayed from a graph, many times, always the same bits."""
+    b = Batch((2000, 900, 70), (300, 1, 70), 2, 16, seed=33)
+    _, _, rope = rotary()
+    host, cache = b.cache8()
+    sel, cnt = selection(b, 6)
+    sel, cnt, kc = sel.cuda(), cnt.cuda(), b.kc.cuda()
+    state = (cache.k_pool, cache.v_pool, cache.kc_pool, cache.k_scale, cache.v_scale)
+    start = [t.clone() for t in state]
+    q_rot, out = torch.empty_like(b.dq), torch.empty_like(b.dq)
+    lse = torch.empty((b.T, b.hq), device="cuda")
+    ws = torch.zeros(dsa.decode_workspace_size(b.T, b.hq, b.hkv, 6), dtype=torch.uint8, device="cuda")
+
+    def both(decode):
+        dsa.kv_append_fp8(cache, b.seqs, b.queries.cu_q, b.dk, b.dv, kc, rope, queries=b.queries, q=b.dq, q_out=q_rot,
+                          dev_err=b.err)
+        if decode:
+            dsa.sparse_attn_decode_fp8(cache, b.seqs, b.queries, q_rot, sel, cnt, out=out, lse=lse, workspace=ws,
+                                       dev_err=b.err)
+        else:
+            dsa.sparse_attn_prefill_fp8(cache, b.seqs, b.queries, q_rot, sel, cnt, out=out, lse=lse, dev_err=b.err)
+
+    def restore():
+        for t, old in zip(state, start):
+            t.copy_(old)
+        q_rot.zero_()
+        out.zero_()
+        torch.cuda.synchronize()
+
+    for decode in (True, False):
+        restore()
+        both(decode)
+        torch.cuda.synchronize()
+        want = out.clone(), lse.clone()
+        few = torch.tensor([0, 150, 299, 300, 301, 370])
+        (k, ks), (v, vs) = ((cache.k_pool, cache.k_scale), (cache.v_pool, cache.v_scale))
+        w, wl, otol, _ = ref.attention(q_rot.cpu()[few].double(), ref.stored(k.cpu(), ks.cpu()),
+                                       ref.stored(v.cpu(), vs.cpu()), b.table, b.block, [b.seq[i] for i in few],
+                                       b.pos[few].tolist(), sel.cpu()[few], cnt.cpu()[few], 1 / math.sqrt(128))
+        assert bool(((out.cpu()[few].double() - w).abs() <= otol).all())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            both(decode)
+        for i in range(20):
+            restore()
+            graph.replay() if i % 2 else both(decode)
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert int(b.err) == 0
+
+
+def test_two_batches_on_two_streams(cuda_device):
+    """Independent batches in flight on streams of their own, outputs allocated by the calls:
+    the results of each alone."""
+    batches = []
+    for i in range(2):
+        b = Batch((3000, 500 + i), (1, 1), 2, 16, seed=50 + i)
+        host, cache = b.cache8()
+        sel, cnt = selection(b, 8)
+        batches.append((b, cache, torch.randn(b.T, b.hq, 128, generator=b.gen).bfloat16().cuda(), sel.cuda(), cnt.cuda()))
+    _, _, rope = rotary()
+
+    def work(b, cache, q, sel, cnt, stream=None):
+        r = dsa.kv_append_fp8(cache, b.seqs, b.queries.cu_q, b.dk, b.dv, None, rope, queries=b.queries, q=q,
+                              stream=stream)
+        return r, dsa.sparse_attn_decode_fp8(cache, b.seqs, b.queries, r, sel, cnt, stream=stream)
+
+    alone = []
+    for a in batches:
+        r, (out, lse) = work(*a)
+        torch.cuda.synchronize()
+        alone.append((r.clone(), out.clone(), lse.clone()))
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    kept = []
+    for _ in range(20):
+        for a, s in zip(batches, streams):
+            kept.append(work(*a, stream=s))
+    torch.cuda.synchronize()
+    for i, (r, (out, lse)) in enumerate(kept):
+        want = alone[i % 2]
+        assert torch.equal(r, want[0]) and torch.equal(out, want[1]) and torch.equal(lse, want[2])
+
+
+def test_binding_refuses_what_would_read_out_of_bounds(cuda_device):
+    b = Batch((70, 90), (3, 1), 2, 4, seed=60)
+    _, cache = b.cache8()
+    _, _, rope = rotary()
+    sel, cnt = selection(b, 2)
+    q = b.dq
+    short = dsa.QueryBatch(b.queries.cu_q[:2].clone(), b.queries.q_pos)
+    with pytest.raises(ValueError, match="cu_q"):
+        dsa.sparse_attn_decode_fp8(cache, b.seqs, short, q, sel.cuda(), cnt.cuda())
+    with pytest.raises(ValueError, match="k_max"):
+        dsa.sparse_attn_decode_fp8(cache, b.seqs, b.queries, q, sel[:2].cuda(), cnt.cuda())
+    with pytest.raises(ValueError, match="lse"):
+        dsa.sparse_attn_decode_fp8(cache, b.seqs, b.queries, q, sel.cuda(), cnt.cuda(), lse=torch.empty(1, 4, device="cuda"))
+    with pytest.raises(ValueError, match="must be"):
+        dsa.sparse_attn_decode_fp8(cache, b.seqs, b.queries, q.half(), sel.cuda(), cnt.cuda())
+    with pytest.raises(ValueError, match="v_new"):
+        dsa.kv_append_fp8(cache, b.seqs, b.queries.cu_q, b.dk, b.dv[:2])
+    with pytest.raises(ValueError, match="cu_new"):
+        dsa.kv_append_fp8(cache, b.seqs, b.queries.cu_q[:2].clone(), b.dk, b.dv)
+    with pytest.raises(ValueError, match="needs v_new"):
+        dsa.kv_append_fp8(cache, b.seqs, b.queries.cu_q, b.dk, None)
+    with pytest.raises(ValueError, match="contiguous"):
+        dsa.kv_append_fp8(cache, b.seqs, b.queries.cu_q, b.dk.transpose(1, 2).contiguous().transpose(1, 2), b.dv)
+    with pytest.raises(ValueError, match="pos_new"):
+        dsa.kv_append_fp8(cache, b.seqs, b.queries.cu_q, b.dk, b.dv, None, rope, pos_new=b.queries.q_pos[:2])
+    with pytest.raises(ValueError, match="q_out"):
+        dsa.kv_append_fp8(cache, b.seqs, b.queries.cu_q, b.dk, b.dv, None, rope, queries=b.queries, q=q,
+                          q_out=q[:, :2].contiguous())
+    with pytest.raises(ValueError, match="CUDA tensors only"):
+        dsa.kv_append_fp8(cache, b.seqs, b.queries.cu_q, b.dk.cpu(), b.dv)
+    with pytest.raises(TypeError):
+        dsa.sparse_attn_decode(cache, b.seqs, b.queries, q, sel.cuda(), cnt.cuda())
+    with pytest.raises(dsa.DsaError):
+        dsa.sparse_attn_decode_fp8(cache, b.seqs, b.queries, q, sel.cuda(), cnt.cuda(),
+                                   workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+
+
 
 @pytest.mark.parametrize("decode,fused", [(True, False), (True, True), (False, True), (False, False)],
                          ids=["decode", "decode_fused_select", "prefill_fused_select", "prefill"])

@@ -157,8 +157,10 @@ def test_binding_refuses_host_tensors_and_the_wrong_cache():
     with pytest.raises(TypeError):
         dsa.kv_append_fp8(c16, s, q.cu_q, row, row)
     # a bf16 append would write two bytes per code: the 8-bit cache is not taken for a bf16 one
-    with pytest.raises(Exception):
+    with pytest.raises(TypeError, match="bf16 PagedKVCache"):
         dsa.kv_append(c8, s, q.cu_q, row, row)
+    with pytest.raises(TypeError, match="bf16 PagedKVCache"):
+        dsa.sparse_attn_prefill(c8, s, q, row, sel, cnt)
     for kw in (dict(overlap_append=True, fused_select=True), dict(fused_decode=True)):
         with pytest.raises(ValueError, match="rotated already"):
             dsa.step(c8, s, q, k_new=row, v_new=row, kc_new=None, q=row, q_idx=None, w=None, k_per_seq=None, k_max=1,
