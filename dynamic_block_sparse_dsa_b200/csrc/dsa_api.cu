@@ -148,7 +148,7 @@ void attn_schedule_fp8(AttnArgs &a, bool allow_split) {
     // chunk 2.63 ms, 333 queries 113 us; with 8 warps 3.00 ms, 125 us); 8 divide a
     // decode batch better (8 long contexts 11.6 us, 64 short ones 26.5 us; with 12
     // warps 12.7 us, 29.5 us)
-    const int warps = pairs < C * fp8_max_warps(1) || a.group > 8 ? 8 : fp8_max_warps(1);
+    const int warps = pairs < C * kFp8ManyWarps || a.group > 8 ? kFp8Warps : kFp8ManyWarps;
     const long long W = C * warps;
     a.warps = warps;
     const long long tiles = (long long)a.k_max << a.tile_shift;

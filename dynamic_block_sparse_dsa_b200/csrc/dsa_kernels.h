@@ -239,9 +239,9 @@ int check_decode_attn_args(const dsa_kv_cache *cache, const dsa_seqs *seqs, cons
                            int32_t k_max, float sm_scale, void *out, float *lse);
 // largest grid the attention kernel uses (sizes the partial-state workspace)
 constexpr int kAttnMaxCtas = 256;
-// most warps per CTA of the E4M3 attention kernel, for nt tiles of 8 query heads: as
-// many as the registers allow (168 and 255 a thread)
-constexpr int fp8_max_warps(int nt) { return nt == 1 ? 12 : 8; }
+// warps per CTA of the E4M3 attention kernel: 8, or 12 (168 registers a thread)
+// for groups of <= 8 heads with a pair for every warp
+constexpr int kFp8Warps = 8, kFp8ManyWarps = 12;
 // floats per partial-state row: o[128], m, l, padded to a 16-byte multiple
 constexpr int kAttnPartStride = 132;
 

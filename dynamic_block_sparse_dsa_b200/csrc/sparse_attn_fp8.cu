@@ -78,7 +78,7 @@ struct Plan {
           words(bars + warps * kSlots * 8),                    // never, last
           bytes(words + 8 + 1024) {}                           // + base alignment slack
 };
-static_assert(Plan(fp8_max_warps(1)).bytes <= 227 * 1024, "shared memory");
+static_assert(Plan(kFp8ManyWarps).bytes <= 227 * 1024, "shared memory");
 static_assert(16 * kMergeStride * 4 <= kRingBytes, "a warp's state fits its ring");
 
 using unit_t = uint32_t;
@@ -128,6 +128,12 @@ __device__ __forceinline__ float max_nan(float x, float y) {
     float z;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
     return z;
+}
+
+__device__ __forceinline__ float max3_nan(float x, float y, float z) {
+    float w;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(w) : "f"(x), "f"(y), "f"(z));
+    return w;
 }
 
 // natural log-sum-exp from a base-2 maximum and sum; -inf for an empty row, NaN kept
@@ -245,8 +251,10 @@ __device__ __forceinline__ void scores(uint32_t tk, const uint32_t (&qb)[8][NT][
 // fragments pb[k-step of 16 tokens].
 template <int NT>
 __device__ __forceinline__ void softmax(float (&sc)[4][NT][4], const float (&mul)[NT][2], float s_k, int lim,
-                                        State<NT> &st, float (&alpha)[NT][2], uint32_t (&pb)[4][NT][2]) {
+                                        State<NT> &st, uint32_t (&pb)[4][NT][2]) {
     const int g = (threadIdx.x & 31) >> 2;
+    float alpha[NT][2];
+    bool moved = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const float f[2] = {mul[nt][0] * s_k, mul[nt][1] * s_k};
@@ -265,7 +273,7 @@ __device__ __forceinline__ void softmax(float (&sc)[4][NT][4], const float (&mul
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k & 1] = max_nan(mx[k & 1], sc[mt][nt][k]);
+            for (int k = 0; k < 2; ++k) mx[k] = max3_nan(mx[k], sc[mt][nt][k], sc[mt][nt][k + 2]);
         float ref[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -278,6 +286,7 @@ __device__ __forceinline__ void softmax(float (&sc)[4][NT][4], const float (&mul
             const float m_new = fmaxf(st.m[nt][h], mx[h]);
             ref[h] = m_new == -INFINITY ? 0.f : m_new;   // nothing visible yet: every weight is 2^-inf = 0
             alpha[nt][h] = exp2_fast(st.m[nt][h] - ref[h]);
+            moved |= m_new != st.m[nt][h];
             st.m[nt][h] = m_new;
         }
         float rs[2] = {0.f, 0.f};
@@ -294,13 +303,22 @@ __device__ __forceinline__ void softmax(float (&sc)[4][NT][4], const float (&mul
         st.l[nt][0] = st.l[nt][0] * alpha[nt][0] + rs[0];
         st.l[nt][1] = st.l[nt][1] * alpha[nt][1] + rs[1];
     }
+    // past the first tiles the maxima rarely move, and O keeps its scale
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int dm = 0; dm < 8; ++dm)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) st.o[dm][nt][k] *= alpha[nt][k & 1];
+    }
 }
 
-// O^T = alpha O^T + s_v (V^T P^T) for one V tile; the tile's product is formed
-// on its own, since every tile has its own scale
+// O^T += s_v (V^T P^T) for one V tile; the tile's product is formed on its own,
+// since every tile has its own scale
 template <int NT>
 __device__ __forceinline__ void weigh(uint32_t tv, float s_v, const uint32_t (&pb)[4][NT][2],
-                                      const float (&alpha)[NT][2], State<NT> &st) {
+                                      State<NT> &st) {
     const int lane = threadIdx.x & 31;
     // the token whose row this lane addresses: row 4 c + i of a matrix is token
     // 2 c + (i & 1) + 8 (i >> 1) of its 16
@@ -327,8 +345,7 @@ __device__ __forceinline__ void weigh(uint32_t tv, float s_v, const uint32_t (&p
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                st.o[dm][nt][k] = fmaf(pv[nt][k], s_v, st.o[dm][nt][k] * alpha[nt][k & 1]);
+            for (int k = 0; k < 4; ++k) st.o[dm][nt][k] = fmaf(pv[nt][k], s_v, st.o[dm][nt][k]);
     }
 }
 
@@ -340,12 +357,12 @@ struct Tile {
 
 }  // namespace
 
-// NT: query-head n-tiles of 8 (the GQA group is <= 8 * NT)
-template <int NT>
-__global__ void __launch_bounds__(fp8_max_warps(NT) * 32, 1)
+// NT: query-head n-tiles of 8 (the GQA group is <= 8 * NT); kWarps: warps per CTA
+template <int NT, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, 1)
 sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, AttnArgs a) {
-    const int threads = blockDim.x, warps = threads >> 5;
-    const Plan plan(warps);
+    constexpr int warps = kWarps, threads = kWarps * 32;
+    constexpr Plan plan(kWarps);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (base - raw);
@@ -467,30 +484,17 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         d.kvh = __shfl_sync(0xffffffffu, l_kvh, src);
         return d;
     };
-    // ---- the ring: K and V tiles in turn, K of tile i the 2i-th copy, V the next;
-    // copy n goes to slot n % kSlots as soon as copy n - kSlots is read
-    int in_flight = 0, slot_in = 0, slot = 0;   // copies not yet waited for; next slot to fill, to read
-    uint32_t phase = 0;                         // of the slot to read
-    auto issue = [&](const CUtensorMap *tm, const Tile &d) {
-        if (d.x >= 0) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bars + 8 * slot_in, kTileBytes);
-                tma_load_3d(ring + slot_in * kTileBytes, tm, 0, d.kvh, d.row, bars + 8 * slot_in);
-            }
-            slot_in = slot_in + 1 == kSlots ? 0 : slot_in + 1;
-            ++in_flight;
+    // ---- the ring: every K tile in slot 0, every V tile in slot 1, each refilled
+    // as soon as it is read
+    auto issue = [&](int slot, const Tile &d) {
+        if (d.x >= 0 && lane == 0) {
+            mbar_arrive_expect_tx(bars + 8 * slot, kTileBytes);
+            tma_load_3d(ring + slot * kTileBytes, slot ? &tm_v : &tm_k, 0, d.kvh, d.row, bars + 8 * slot);
         }
     };
-    uint32_t tile = 0;   // address of the copy waited for
-    auto arrived = [&]() {
-        if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * slot, phase, s_never))) return false;
-        tile = ring + slot * kTileBytes;
-        --in_flight;
-        if (++slot == kSlots) {
-            slot = 0;
-            phase ^= 1;
-        }
-        return true;
+    uint32_t phase = 0;   // of the current tile, in both slots
+    auto arrived = [&](int slot) {
+        return __all_sync(0xffffffffu, mbar_wait(bars + 8 * slot, phase, s_never)) != 0;
     };
 
     uint32_t qb[8][NT][2];
@@ -498,26 +502,27 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     State<NT> st;
     Tile cur = next();
     pdl_wait();
-    issue(&tm_k, cur);
-    issue(&tm_v, cur);
+    issue(0, cur);
+    issue(1, cur);
     Tile nxt = next();
-    bool dead = false;
+    bool dead = false, dead_behind_k = false;   // a wait gave up; behind the next K tile's copy
     // the warp's tiles before place x_end, all of one pair at position p
     auto run = [&](unit_t x_end, int p) {
         while (!dead && cur.x >= 0 && (unit_t)cur.x < x_end) {
-            float sc[4][NT][4], alpha[NT][2];
+            float sc[4][NT][4];
             uint32_t pb[4][NT][2];
             // one address for the whole warp; the values are used after the first product
             const size_t si = (size_t)(cur.row >> 6) * a.num_kv_heads + cur.kvh;
             const float s_k = ld_ordered_cg(a.k_scale + si), s_v = ld_ordered_cg(a.v_scale + si);
-            if (!arrived()) { dead = true; break; }
-            scores<NT>(tile, qb, sc);
+            if (!arrived(0)) { dead = true; break; }
+            scores<NT>(ring, qb, sc);
             __syncwarp();
-            issue(&tm_k, nxt);
+            issue(0, nxt);
             const int lim = p - cur.blk * kBlockSize;   // >= 63 but in the query's own tile
-            softmax<NT>(sc, mul, s_k, lim, st, alpha, pb);
+            softmax<NT>(sc, mul, s_k, lim, st, pb);
             const Tile after = next();
-            if (!arrived()) { dead = true; break; }
+            if (!arrived(1)) { dead = dead_behind_k = true; break; }
+            const uint32_t tile = ring + kTileBytes;
             if (lim < kBlockSize - 1) {
                 // slots past the query's position hold whatever the cache had there;
                 // a zero weight times a NaN is NaN, so their value rows are cleared
@@ -525,11 +530,12 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                     st_shared_zero16(tile + swz128(lim + 1 + (e >> 3), e & 7));
                 __syncwarp();
             }
-            weigh<NT>(tile, s_v, pb, alpha, st);
+            weigh<NT>(tile, s_v, pb, st);
             // generic-proxy stores (the cleared rows) before the TMA refills the slot
             if (lim < kBlockSize - 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            issue(&tm_v, nxt);
+            issue(1, nxt);
+            phase ^= 1;
             cur = nxt;
             nxt = after;
         }
@@ -681,12 +687,10 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         // limit) before the CTA's shared memory goes to the next one
         if (lane == 0) {
             set_err(a.dev_err, DSA_DEV_ERR_WAIT);
-            for (; in_flight > 0; --in_flight) {
+            // the current tile's phase of each slot, and the next tile's where it was issued
+            for (int slot = 0; slot < kSlots; ++slot) {
                 mbar_wait(bars + 8 * slot, phase, s_never);
-                if (++slot == kSlots) {
-                    slot = 0;
-                    phase ^= 1;
-                }
+                if (slot == 0 && dead_behind_k && nxt.x >= 0) mbar_wait(bars, phase ^ 1, s_never);
             }
         }
         __syncwarp();
@@ -727,20 +731,21 @@ cudaError_t pool_map(CUtensorMap &m, const void *pool, const AttnArgs &a) {
                : cudaErrorInvalidValue;
 }
 
-template <int NT>
+template <int NT, int kWarps>
 cudaError_t launch(const AttnArgs &a, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t stream) {
     // the shared-memory opt-in, once per device
     static std::atomic<unsigned long long> done{0};
+    constexpr int bytes = Plan(kWarps).bytes;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(done.load() >> dev & 1)) {
-        e = cudaFuncSetAttribute(sparse_attn_fp8_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Plan(fp8_max_warps(NT)).bytes);
+        e = cudaFuncSetAttribute(sparse_attn_fp8_kernel<NT, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) done.fetch_or(1ull << dev);
     }
-    return launch_pdl(sparse_attn_fp8_kernel<NT>, dim3(a.num_ctas), dim3(a.warps * 32), (size_t)Plan(a.warps).bytes, stream, k, v, a);
+    return launch_pdl(sparse_attn_fp8_kernel<NT, kWarps>, dim3(a.num_ctas), dim3(kWarps * 32), (size_t)bytes, stream, k,
+                      v, a);
 }
 
 }  // namespace
@@ -750,7 +755,8 @@ cudaError_t launch_sparse_attn_fp8(const AttnArgs &a, cudaStream_t stream) {
     cudaError_t e = pool_map(k, a.k_pool, a);
     if (e == cudaSuccess) e = pool_map(v, a.v_pool, a);
     if (e != cudaSuccess) return e;
-    return a.group <= 8 ? launch<1>(a, k, v, stream) : launch<2>(a, k, v, stream);
+    if (a.group > 8) return launch<2, kFp8Warps>(a, k, v, stream);
+    return a.warps == kFp8Warps ? launch<1, kFp8Warps>(a, k, v, stream) : launch<1, kFp8ManyWarps>(a, k, v, stream);
 }
 
 }  // namespace dsa
