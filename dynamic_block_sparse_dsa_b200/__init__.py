@@ -40,6 +40,7 @@ from typing import Optional
 import torch
 
 from . import _lib
+from ._args import HEAD_DIM, _at, _rows, _wrong_device
 from ._lib import DsaError, load
 
 __all__ = [
@@ -52,7 +53,6 @@ __all__ = [
 ]
 
 BLOCK_SIZE = 64
-HEAD_DIM = 128
 IDX_DIM = 64
 TILE = 64   # tokens that share one scale of the 8-bit cache
 
@@ -80,24 +80,6 @@ def _stream(stream) -> ctypes.c_void_p:
 def _expect(t: torch.Tensor, dtype, name):
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-
-
-def _at(t: torch.Tensor, dtype, dev: int, name: str) -> int:
-    """Address of a contiguous ``dtype`` tensor on device ``dev``."""
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    at = t.get_device()
-    if at != dev:
-        _wrong_device(at, dev, name)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _wrong_device(at: int, dev: int, name: str):
-    if at < 0:
-        raise ValueError("dynamic_block_sparse_dsa_b200 works on CUDA tensors only (no CPU path)")
-    raise ValueError(f"{name} is on cuda:{at}, the call's other tensors on cuda:{dev}")
 
 
 def _current(t: torch.Tensor) -> int:
@@ -177,21 +159,22 @@ class PagedKVCacheFP8:
 
     def packed(self, dev: int) -> bytes:
         """The C description (dsa_kv_cache_fp8) of tensors on device ``dev``."""
-        kp, vp, kc = self.k_pool, self.v_pool, self.kc_pool
-        if kp.dtype not in _CODES or vp.dtype not in _CODES:
-            raise ValueError(f"k_pool and v_pool must hold E4M3 codes, got {kp.dtype} and {vp.dtype}")
+        kp, vp, kc, ks, vs = self.k_pool, self.v_pool, self.kc_pool, self.k_scale, self.v_scale
+        code = kp.dtype
+        if code not in _CODES:
+            raise ValueError(f"k_pool and v_pool must hold E4M3 codes, got {code}")
         n, bs, hkv, d = kp.shape
         if vp.shape != kp.shape:
             raise ValueError("k_pool and v_pool differ in shape")
         pages, idx_dim = kc.shape
         if kc.element_size() != 1 or pages != n:
             raise ValueError("kc_pool must hold one byte per element and one row per page")
-        tiles = (n, bs // TILE, hkv)
-        if self.k_scale.shape != tiles or self.v_scale.shape != tiles:
-            raise ValueError(f"k_scale and v_scale must be {list(tiles)}")
-        return _lib.pack_cache_fp8(_at(kp, kp.dtype, dev, "k_pool"), _at(vp, vp.dtype, dev, "v_pool"),
-                                   _at(kc, kc.dtype, dev, "kc_pool"), _at(self.k_scale, torch.float32, dev, "k_scale"),
-                                   _at(self.v_scale, torch.float32, dev, "v_scale"), n, bs, hkv, d, idx_dim)
+        scales = n * (bs // TILE) * hkv
+        if ks.numel() != scales or vs.numel() != scales:
+            raise ValueError(f"k_scale and v_scale must be {[n, bs // TILE, hkv]}")
+        return _lib.pack_cache_fp8(_at(kp, code, dev, "k_pool"), _at(vp, code, dev, "v_pool"),
+                                   _at(kc, kc.dtype, dev, "kc_pool"), _at(ks, torch.float32, dev, "k_scale"),
+                                   _at(vs, torch.float32, dev, "v_scale"), n, bs, hkv, d, idx_dim)
 
     def index_ctype(self) -> _lib.KvCacheC:
         """What the indexer and selection calls read: the coarse keys and the sizes."""
@@ -286,26 +269,6 @@ def kv_append(cache: PagedKVCache, seqs: SeqBatch, cu_new: torch.Tensor, k_new: 
         _ptr(kc_new), _ptr(dev_err), _stream(stream)))
 
 
-def _rows(t: torch.Tensor, dev: int, name: str):
-    """(address, tokens, heads, elements from one token to the next) of bf16
-    [tokens][heads][128] rows; only the tokens may be apart (slices of a packed
-    projection)."""
-    if t.dtype is not torch.bfloat16:
-        raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
-    at = t.get_device()
-    if at != dev:
-        _wrong_device(at, dev, name)
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens][heads][{HEAD_DIM}], got {list(t.shape)}")
-    n, heads, d = t.shape
-    s0, s1, s2 = t.stride()
-    if d != HEAD_DIM or s2 != 1 or (s1 != HEAD_DIM and heads > 1):
-        raise ValueError(f"{name} must be [tokens][heads][{HEAD_DIM}] with each token's heads contiguous, got "
-                         f"{list(t.shape)} with strides {list(t.stride())}")
-    # a single token has no next one; torch may give it any stride
-    return t.data_ptr(), n, heads, s0 if n > 1 else heads * HEAD_DIM
-
-
 def _positions(pos: Optional[torch.Tensor], axes: int, n: int, dev: int, name: str) -> int:
     if pos is None:
         return 0
@@ -319,20 +282,20 @@ def _append_rope(fn: str, cache, seqs: SeqBatch, cu_new, k_new, v_new, kc_new, r
     lib = load()
     dev = _current(cache.k_pool)
     axes = 1 if rope is None else rope.num_axes
-    fresh = _NOTHING_NEW
+    fresh, hkv = _NOTHING_NEW, cache.k_pool.shape[2]
     if k_new is not None and len(k_new):
         if v_new is None or cu_new is None:
             raise ValueError("k_new needs v_new and cu_new")
         k, total, heads, ks = _rows(k_new, dev, "k_new")
         v, v_total, v_heads, vs = _rows(v_new, dev, "v_new")
-        if heads != cache.num_kv_heads or v_heads != heads or v_total != total:
-            raise ValueError(f"k_new and v_new must be [{total}][{cache.num_kv_heads}][{HEAD_DIM}]")
+        if heads != hkv or v_heads != hkv or v_total != total:
+            raise ValueError(f"k_new and v_new must be [{total}][{hkv}][{HEAD_DIM}]")
         if cu_new.numel() != seqs.seq_lens.numel() + 1:
             raise ValueError("cu_new must have one entry more than there are sequences")
         kc = 0
         if kc_new is not None:
-            if kc_new.element_size() != 1 or kc_new.shape != (total, cache.kc_pool.shape[1]):
-                raise ValueError(f"kc_new must hold one byte per element, [{total}][{cache.kc_pool.shape[1]}]")
+            if kc_new.element_size() != 1 or kc_new.numel() != total * IDX_DIM:
+                raise ValueError(f"kc_new must hold one byte per element, [{total}][{IDX_DIM}]")
             kc = _at(kc_new, kc_new.dtype, dev, "kc_new")
         fresh = _lib.pack_new_tokens(_at(cu_new, torch.int32, dev, "cu_new"), total, k, v, ks, vs, kc,
                                      _positions(pos_new, axes, total, dev, "pos_new"))

@@ -126,6 +126,8 @@ def load():
     """Load libdsa.so (building it first if it is missing or older than its
     sources and nvcc is available).  Raises if the library cannot be loaded."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

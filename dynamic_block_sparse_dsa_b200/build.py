@@ -15,6 +15,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdsa.so")
+ARGS_SRC = os.path.join(CSRC, "tensor_args.cpp")
+ARGS_LIB = os.path.join(PKG, "_tensor_args.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -41,8 +43,37 @@ def is_stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
+def build_tensor_args(force: bool = False) -> bool:
+    """Compile the binding's native tensor reader beside libdsa.so.  The binding
+    does the same in Python without it, so a failure here is only reported."""
+    if not force and os.path.exists(ARGS_LIB) and os.path.getmtime(ARGS_LIB) >= os.path.getmtime(ARGS_SRC):
+        return True
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    tmp = ARGS_LIB + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[a for i in inc for a in ("-isystem", i)],
+           "-o", tmp, ARGS_SRC, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        sys.stderr.write(f"tensor_args.cpp not built: {e}\n")
+        return False
+    if r.returncode != 0:
+        sys.stderr.write(f"tensor_args.cpp not built ({r.returncode}):\n{r.stderr[-2000:]}\n")
+        return False
+    os.replace(tmp, ARGS_LIB)
+    return True
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every csrc/*.cu into one shared library (static cudart)."""
+    """Compile every csrc/*.cu into one shared library (static cudart), and the
+    binding's tensor reader."""
+    build_tensor_args(force)
     if not force and not is_stale():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"

@@ -195,6 +195,36 @@ def test_binding_refuses_mismatched_shapes():
         dsa._at(row, torch.bfloat16, 0, "row") if row.get_device() >= 0 else dsa._wrong_device(1, 0, "row")
 
 
+def test_native_tensor_reader_answers_as_the_python_one():
+    """Same addresses and strides, same refusals, for contiguous and sliced, empty and
+    single-token, wrongly typed and wrongly shaped tensors (on the CPU: device -1)."""
+    from dynamic_block_sparse_dsa_b200 import _args
+    from dynamic_block_sparse_dsa_b200 import build as b
+    if not b.build_tensor_args():
+        pytest.skip("no C++ compiler here")
+    native = pytest.importorskip("dynamic_block_sparse_dsa_b200._tensor_args")
+    native.use(_args.py_at, _args.py_rows)
+
+    def both(f, g, *a):
+        got = []
+        for h in (f, g):
+            try:
+                got.append(h(*a))
+            except Exception as e:
+                got.append((type(e), str(e)))
+        assert got[0] == got[1], (a, got)
+        return got[0]
+
+    x = torch.zeros(5, 6, 128, dtype=torch.bfloat16)
+    for t in (x, x[:, 1:3], x[:1], x[:1, 2:3], x[:, :, :64], x.transpose(0, 1), x[::2], x[:0], x.float(), x[0], x[..., ::2]):
+        both(native.rows, _args.py_rows, t, -1, "x")
+        both(native.at, _args.py_at, t, torch.bfloat16, -1, "x")
+        both(native.at, _args.py_at, t, torch.bfloat16, 0, "x")
+        both(native.rows, _args.py_rows, t, 0, "x")
+    assert both(native.rows, _args.py_rows, x[:, 1:3], -1, "x") == (x.data_ptr() + 256, 5, 2, 768)
+    assert both(native.at, _args.py_at, None, torch.int32, -1, "x")[0] is AttributeError
+
+
 def test_packed_structs_have_the_c_layout():
     """The packed bytes are the ctypes structures' bytes (up to the padding at their end)."""
     def same(packed, c):
