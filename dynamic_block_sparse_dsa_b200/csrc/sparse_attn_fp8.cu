@@ -504,6 +504,17 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     pdl_wait();
     issue(0, cur);
     issue(1, cur);
+    // a tile's scales (one address for the whole warp) are loaded a tile ahead: they
+    // come from memory as slowly as the codes do
+    auto scales_of = [&](const Tile &d, float &k, float &v) {
+        if (d.x >= 0) {
+            const size_t i = (size_t)(d.row >> 6) * a.num_kv_heads + d.kvh;
+            k = ld_ordered_cg(a.k_scale + i);
+            v = ld_ordered_cg(a.v_scale + i);
+        }
+    };
+    float s_k = 0.f, s_v = 0.f;
+    scales_of(cur, s_k, s_v);
     Tile nxt = next();
     bool dead = false, dead_behind_k = false;   // a wait gave up; behind the next K tile's copy
     // the warp's tiles before place x_end, all of one pair at position p
@@ -511,9 +522,8 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         while (!dead && cur.x >= 0 && (unit_t)cur.x < x_end) {
             float sc[4][NT][4];
             uint32_t pb[4][NT][2];
-            // one address for the whole warp; the values are used after the first product
-            const size_t si = (size_t)(cur.row >> 6) * a.num_kv_heads + cur.kvh;
-            const float s_k = ld_ordered_cg(a.k_scale + si), s_v = ld_ordered_cg(a.v_scale + si);
+            float nxt_k = 0.f, nxt_v = 0.f;
+            scales_of(nxt, nxt_k, nxt_v);
             if (!arrived(0)) { dead = true; break; }
             scores<NT>(ring, qb, sc);
             __syncwarp();
@@ -538,6 +548,8 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             phase ^= 1;
             cur = nxt;
             nxt = after;
+            s_k = nxt_k;
+            s_v = nxt_v;
         }
     };
 
