@@ -40,7 +40,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._args import HEAD_DIM, _at, _rows, _wrong_device
+from ._args import HEAD_DIM, _at, _rows, _wrong_device, native as _native
 from ._lib import DsaError, load
 
 __all__ = [
@@ -281,6 +281,21 @@ def _append_rope(fn: str, cache, seqs: SeqBatch, cu_new, k_new, v_new, kc_new, r
                  dev_err, stream):
     lib = load()
     dev = _current(cache.k_pool)
+    if q is not None and q_out is None and rope is not None and queries is not None:
+        with _on(stream):
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if _native is not None and lib is _lib._lib:   # a recorder wants the marshalled arguments
+        f8 = isinstance(cache, PagedKVCacheFP8)
+        r, qs = rope or _NO_ROPE, queries or _NO_QUERIES
+        rc = _native.append(
+            _lib.ADDRESS[fn], dev, _raw_stream(stream, dev), cache.k_pool, cache.v_pool, cache.kc_pool,
+            cache.k_scale if f8 else None, cache.v_scale if f8 else None, seqs.block_table, seqs.seq_lens, cu_new, k_new,
+            v_new, kc_new, pos_new, r.inv_freq, r.pair_axis, r.interleaved, r.num_axes, r.scale, qs.cu_q, qs.q_pos, q,
+            pos_q, q_out, dev_err)
+        if rc is not None:
+            if rc:
+                _lib.check(fn, rc)
+            return q_out
     axes = 1 if rope is None else rope.num_axes
     fresh, hkv = _NOTHING_NEW, cache.k_pool.shape[2]
     if k_new is not None and len(k_new):
@@ -306,10 +321,7 @@ def _append_rope(fn: str, cache, seqs: SeqBatch, cu_new, k_new, v_new, kc_new, r
         qp, n, heads, qs = _rows(q, dev, "q")
         if n != queries.total_q:
             raise ValueError(f"q has {n} rows for {queries.total_q} queries")
-        if q_out is None:
-            with _on(stream):
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif q_out.shape != q.shape:
+        if q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
         rows = _lib.pack_query_rows(qp, qs, heads, _positions(pos_q, axes, n, dev, "pos_q"),
                                     _at(q_out, torch.bfloat16, dev, "q_out"))
@@ -323,6 +335,7 @@ def _append_rope(fn: str, cache, seqs: SeqBatch, cu_new, k_new, v_new, kc_new, r
 
 
 _NOTHING_NEW = _lib.pack_new_tokens(0, 0, 0, 0, 0, 0, 0, 0)
+_NO_ROPE, _NO_QUERIES = Rotary(None), QueryBatch(None, None)
 
 
 def kv_append_rope(cache: PagedKVCache, seqs: SeqBatch, cu_new: Optional[torch.Tensor], k_new: Optional[torch.Tensor],
@@ -584,7 +597,7 @@ def _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, stream
         raise ValueError(f"q must be [{T}][heads][{HEAD_DIM}], got {list(q.shape)}")
     if sel.dim() != 2 or sel.shape[0] != T or cnt.numel() != T:
         raise ValueError(f"sel must be [{T}][k_max] and cnt [{T}]")
-    if queries.cu_q.numel() != seqs.seq_lens.numel() + 1:
+    if queries.cu_q.numel() != seqs.block_table.shape[0] + 1:
         raise ValueError("cu_q must have one entry more than there are sequences")
     if out is None or lse is None:
         with _on(stream):
@@ -599,12 +612,31 @@ def _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, stream
         _at(lse, torch.float32, dev, "lse"))
 
 
+def _attend_native(fn, lib, cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, workspace, dev_err, stream):
+    """The call through the native reader: DSA_OK, or None where the binding's own checks have to look."""
+    if _native is None or lib is not _lib._lib or not isinstance(cache, PagedKVCacheFP8):
+        return None
+    dev = _current(cache.k_pool)
+    rc = _native.attend(_lib.ADDRESS[fn], dev, _raw_stream(stream, dev), cache.k_pool, cache.v_pool, cache.kc_pool,
+                        cache.k_scale, cache.v_scale, seqs.block_table, seqs.seq_lens, queries.cu_q, queries.q_pos, q,
+                        sel, cnt, 1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else float(sm_scale), out, lse, workspace,
+                        dev_err)
+    if rc:
+        _lib.check(fn, rc)
+    return rc
+
+
 def sparse_attn_decode_fp8(cache: PagedKVCacheFP8, seqs: SeqBatch, queries: QueryBatch, q: torch.Tensor,
                            sel: torch.Tensor, cnt: torch.Tensor, sm_scale: Optional[float] = None, out=None, lse=None,
                            workspace: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
                            stream=None):
     """sparse_attn_decode over the 8-bit cache: (out bf16, lse fp32), same workspace."""
     lib = load()
+    if workspace is not None and out is not None and lse is not None:
+        rc = _attend_native("dsa_sparse_attn_decode_fp8", lib, cache, seqs, queries, q, sel, cnt, sm_scale, out, lse,
+                            workspace, dev_err, stream)
+        if rc is not None:
+            return out, lse
     dev, out, lse, args = _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, stream)
     if workspace is None:
         with _on(stream):
@@ -623,6 +655,11 @@ def sparse_attn_prefill_fp8(cache: PagedKVCacheFP8, seqs: SeqBatch, queries: Que
                             lse=None, dev_err: Optional[torch.Tensor] = None, stream=None):
     """sparse_attn_prefill over the 8-bit cache: (out bf16, lse fp32)."""
     lib = load()
+    if out is not None and lse is not None:
+        rc = _attend_native("dsa_sparse_attn_prefill_fp8", lib, cache, seqs, queries, q, sel, cnt, sm_scale, out, lse,
+                            None, dev_err, stream)
+        if rc is not None:
+            return out, lse
     dev, out, lse, args = _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, stream)
     rc = lib.dsa_sparse_attn_prefill_fp8(
         *args, None if dev_err is None else _at(dev_err, torch.int32, dev, "dev_err"), _raw_stream(stream, dev))

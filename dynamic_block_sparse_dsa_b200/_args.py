@@ -53,10 +53,12 @@ def _rows(t: torch.Tensor, dev: int, name: str):
 
 py_at, py_rows = _at, _rows   # what the native reader falls back to
 
+native = None   # the native reader's module
 try:
     from . import _tensor_args
     if _tensor_args.torch_version == torch.__version__.split("+")[0]:
-        _tensor_args.use(py_at, py_rows)
-        _at, _rows = _tensor_args.at, _tensor_args.rows
+        native = _tensor_args
+        native.use(py_at, py_rows)
+        _at, _rows = native.at, native.rows
 except ImportError:   # not built, or built for another Python or torch
     pass

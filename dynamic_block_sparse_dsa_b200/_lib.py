@@ -16,6 +16,7 @@ from . import build as _build
 
 _lock = threading.Lock()
 _lib = None
+ADDRESS = {}   # entry point -> its address, once the library is loaded
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_RANGE, DSA_ERR_WORKSPACE, DSA_ERR_CUDA = range(6)
 DEV_ERR_PAGE, DEV_ERR_POS, DEV_ERR_SEL, DEV_ERR_K, DEV_ERR_WAIT, DEV_ERR_VALUE = 1, 2, 4, 8, 16, 32
@@ -142,6 +143,7 @@ def load():
             f = getattr(lib, name)
             f.argtypes = argt
             f.restype = rest
+            ADDRESS[name] = ctypes.cast(f, c_vp).value
         _lib = lib
         return lib
 

@@ -592,7 +592,37 @@ def test_two_batches_on_two_streams(cuda_device):
         assert torch.equal(r, want[0]) and torch.equal(out, want[1]) and torch.equal(lse, want[2])
 
 
-def test_binding_refuses_what_would_read_out_of_bounds(cuda_device):
+def test_calls_without_the_native_reader(cuda_device, monkeypatch):
+    """The binding's own marshalling makes the same calls as the native reader's."""
+    got = []
+    for native in (True, False):
+        if not native:
+            monkeypatch.setattr(dsa, "_native", None)
+        b, rope, pos, _ = make("three_axes", seed=61)
+        _, cache = b.cache8()
+        q = dsa.kv_append_fp8(cache, b.seqs, b.queries.cu_q, b.dk, b.dv, b.kc.cuda(), rope, pos_new=pos, queries=b.queries,
+                              q=b.dq, pos_q=pos, dev_err=b.err)
+        (_, _), c16 = b.cache16()
+        q16 = dsa.kv_append_rope(c16, b.seqs, b.queries.cu_q, b.dk, b.dv, None, rope, pos_new=pos, queries=b.queries,
+                                 q=b.dq, pos_q=pos, dev_err=b.err)
+        sel, cnt = selection(b, 3)
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        ws = torch.zeros(dsa.decode_workspace_size(b.T, b.hq, b.hkv, 3), dtype=torch.uint8, device="cuda")
+        dsa.sparse_attn_decode_fp8(cache, b.seqs, b.queries, q, sel.cuda(), cnt.cuda(), out=out, lse=lse, workspace=ws,
+                                   dev_err=b.err)
+        out2, lse2 = dsa.sparse_attn_prefill_fp8(cache, b.seqs, b.queries, q, sel.cuda(), cnt.cuda(),
+                                                 out=torch.empty_like(out), lse=torch.empty_like(lse))
+        assert int(b.err) == 0
+        got.append([t.cpu().view(torch.uint8) for t in (q, q16, out, lse, out2, lse2, cache.k_pool, cache.v_pool,
+                                                        cache.k_scale, cache.v_scale, cache.kc_pool, c16.k_pool)])
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("native", [True, False], ids=["native", "python"])
+def test_binding_refuses_what_would_read_out_of_bounds(native, cuda_device, monkeypatch):
+    if not native:
+        monkeypatch.setattr(dsa, "_native", None)
     b = Batch((70, 90), (3, 1), 2, 4, seed=60)
     _, cache = b.cache8()
     _, _, rope = rotary()
@@ -624,9 +654,31 @@ def test_binding_refuses_what_would_read_out_of_bounds(cuda_device):
         dsa.kv_append_fp8(cache, b.seqs, b.queries.cu_q, b.dk.cpu(), b.dv)
     with pytest.raises(TypeError):
         dsa.sparse_attn_decode(cache, b.seqs, b.queries, q, sel.cuda(), cnt.cuda())
-    with pytest.raises(dsa.DsaError):
-        dsa.sparse_attn_decode_fp8(cache, b.seqs, b.queries, q, sel.cuda(), cnt.cuda(),
-                                   workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    ws = torch.zeros(dsa.decode_workspace_size(b.T, b.hq, b.hkv, 2), dtype=torch.uint8, device="cuda")
+    kw = dict(out=out, lse=lse, workspace=ws)
+    for bad in (dict(workspace=ws[:64]), dict(sm_scale=-1.0)):
+        with pytest.raises(dsa.DsaError):
+            dsa.sparse_attn_decode_fp8(cache, b.seqs, b.queries, q, sel.cuda(), cnt.cuda(), **{**kw, **bad})
+    for bad in (dict(out=out.view(b.T, -1)), dict(lse=lse[:2].contiguous()), dict(out=out.float()),
+                dict(dev_err=b.err.long())):
+        with pytest.raises(ValueError):
+            dsa.sparse_attn_decode_fp8(cache, b.seqs, b.queries, q, sel.cuda(), cnt.cuda(), **{**kw, **bad})
+    with pytest.raises(ValueError, match="cu_q"):
+        dsa.sparse_attn_decode_fp8(cache, b.seqs, short, q, sel.cuda(), cnt.cuda(), **kw)
+    with pytest.raises(ValueError, match="k_max"):
+        dsa.sparse_attn_decode_fp8(cache, b.seqs, b.queries, q, sel[:2].cuda(), cnt.cuda(), **kw)
+    with pytest.raises(ValueError, match="seq_lens"):
+        dsa.sparse_attn_decode_fp8(cache, dsa.SeqBatch(b.seqs.block_table, b.seqs.seq_lens[:1]), b.queries, q, sel.cuda(),
+                                   cnt.cuda(), **kw)
+    small = dsa.PagedKVCacheFP8(cache.k_pool, cache.v_pool[:1], cache.kc_pool, cache.k_scale, cache.v_scale)
+    with pytest.raises(ValueError, match="differ in shape"):
+        dsa.sparse_attn_decode_fp8(small, b.seqs, b.queries, q, sel.cuda(), cnt.cuda(), **kw)
+    with pytest.raises(ValueError, match="differ in shape"):
+        dsa.kv_append_fp8(small, b.seqs, b.queries.cu_q, b.dk, b.dv)
+    few = dsa.PagedKVCacheFP8(cache.k_pool, cache.v_pool, cache.kc_pool, cache.k_scale[:1], cache.v_scale)
+    with pytest.raises(ValueError, match="k_scale"):
+        dsa.kv_append_fp8(few, b.seqs, b.queries.cu_q, b.dk, b.dv)
 
 
 
