@@ -83,8 +83,8 @@ struct Plan {
         : ml(warps * kRingBytes),                              // [warp][16] (m, l)
           cuq(ml + warps * 16 * 8),
           bars((cuq + (kMaxSmemSeqs + 1) * 4 + 7) / 8 * 8),
-          words(bars + warps * kSlots * 8),                    // never, last
-          bytes(words + 8 + 1024) {}                           // + base alignment slack
+          words(bars + warps * kSlots * 8),                    // never, last, end of the queries
+          bytes(words + 12 + 1024) {}                          // + base alignment slack
 };
 static_assert(Plan(kFp8ManyWarps).bytes <= 227 * 1024, "shared memory");
 static_assert(16 * kMergeStride * 4 <= kRingBytes, "a warp's state fits its ring");
@@ -377,7 +377,7 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     float *s_ml = reinterpret_cast<float *>(gbase + plan.ml);   // [warp][16][2]
     int *s_cuq = reinterpret_cast<int *>(gbase + plan.cuq);
     volatile int *s_never = reinterpret_cast<volatile int *>(gbase + plan.words);   // stays 0: no abort flag
-    volatile int *s_last = s_never + 1;
+    volatile int *s_last = s_never + 1, *s_end = s_never + 2;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
     const uint32_t ring = base + warp * kRingBytes, bars = base + plan.bars + warp * kSlots * 8;
     const int G = a.group, T = a.total_q;
@@ -397,6 +397,8 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     const bool cached = a.num_seqs + 1 <= kMaxSmemSeqs;
     if (cached)
         for (int i = tid; i <= a.num_seqs; i += threads) s_cuq[i] = __ldg(a.cu_q + i);
+    // queries behind the last sequence's (a padded batch) are not attended to, their rows not written
+    if (tid == 0) *s_end = __ldg(a.cu_q + a.num_seqs);
     __syncthreads();
 
     const int W = gridDim.x * warps, pairs = T * a.num_kv_heads;
@@ -410,9 +412,9 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         const int i = splits > 1 ? c / splits : own0 / team;
         if (a.warp_rounds * W + i < pairs) {
             tail_pair = a.warp_rounds * W + i;
-            const unit_t part = splits > 1 ? (unit_t)(c - i * splits) : 0u;
-            j_lo = part * K / (unit_t)splits;
-            j_hi = (part + 1) * K / (unit_t)splits;
+            const unsigned long long part = splits > 1 ? c - i * splits : 0;   // times K: past 32 bits
+            j_lo = (unit_t)(part * K / (unsigned)splits);
+            j_hi = (unit_t)((part + 1) * K / (unsigned)splits);
         }
     }
     const unit_t j_first = j_lo + (unit_t)member;
@@ -456,7 +458,8 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 int n_sel = ld_ordered_cg(a.cnt + t);
                 const int b = ld_ordered_cg(a.sel + (size_t)t * a.k_max + j);
                 const int n_vis = (p >> a.block_shift) + 1;
-                if (p < 0 || p >= len || n_vis > a.max_blocks || n_sel < 0 || n_sel > a.k_max) n_sel = 0;
+                if (p < 0 || p >= len || n_vis > a.max_blocks || n_sel < 0 || n_sel > a.k_max || t >= *s_end)
+                    n_sel = 0;
                 if (j < n_sel) {
                     if (b < 0 || b >= n_vis) {
                         err_bits |= DSA_DEV_ERR_SEL;
@@ -566,6 +569,7 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         const int pair = own0 + i * W;
         if (pair >= pairs) break;
         const int kvh = pair / T, t = pair - kvh * T;
+        if (t >= *s_end) continue;
         const size_t row0 = (size_t)t * a.num_q_heads + (size_t)kvh * G;
         st.clear();
         load_queries<NT>(a.q + row0 * kHeadDim, G, a.scale_log2, qb, mul);
@@ -639,6 +643,7 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                     const float4 v = *reinterpret_cast<const float4 *>(mo + w * (kRingBytes / 4));
                     acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
                 }
+            if (t >= *s_end) continue;
             if (splits == 1) {
                 const float inv = inv_of(L);
                 *reinterpret_cast<uint2 *>(a.out + (row0 + r) * kHeadDim + d0) =
@@ -656,7 +661,7 @@ sparse_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             __syncthreads();
             if (*s_last) {
                 const int c0 = c / splits * splits;
-                for (int e = tid; e < G * 32; e += threads) {
+                for (int e = tid; e < (t < *s_end ? G * 32 : 0); e += threads) {
                     const int r = e >> 5, d0 = (e & 31) * 4;
                     float M = -INFINITY, L = 0.f;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

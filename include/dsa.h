@@ -183,7 +183,8 @@ typedef struct {
  * dsa_kv_append_rope -- dsa_kv_append with the keys rotated on the way, and
  * the step's queries rotated in the same launch.  K rows go into the cache
  * rotated, V rows and coarse keys as they are.  rows NULL: no queries (queries
- * is not read either); total_new 0: only the queries.
+ * is not read either); total_new 0: only the queries.  All total_q query rows
+ * are rotated, each by its own position, whatever sequence they belong to.
  * Device errors: those of dsa_kv_append and of the rotation.
  */
 int dsa_kv_append_rope(const dsa_kv_cache *cache, const dsa_seqs *seqs, const dsa_new_tokens *fresh,
@@ -393,6 +394,8 @@ int dsa_sparse_attn_prefill(const dsa_kv_cache *cache, const dsa_seqs *seqs,
  * is rounded), softmax weights are rounded to f16, sums are fp32.  Slots that
  * no query sees (behind its position, or never written) may hold any codes; a
  * NaN in a code, scale or query that a row does use makes its results NaN.
+ * Queries from cu_q[num_seqs] on (a padded batch) belong to no sequence: their
+ * rows of out and lse are left as they were.
  * Device errors: those of the bf16 calls.
  */
 int dsa_sparse_attn_decode_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *seqs, const dsa_queries *queries,

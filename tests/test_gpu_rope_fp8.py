@@ -402,6 +402,38 @@ def test_attention_fp8_rows_without_blocks_and_bad_selections(cuda_device):
     assert int(b.err) == _lib.DEV_ERR_PAGE
 
 
+@pytest.mark.parametrize("lens,n_new,hkv,hq,k", [((300, 500), (4, 3), 2, 8, 4), ((3000,), (1,), 2, 8, 47),
+                                                ((200,) * 700, (1,) * 700, 2, 4, 3)],
+                         ids=["teams", "split_contexts", "pairs_per_warp"])
+def test_attention_fp8_padded_batch(lens, n_new, hkv, hq, k, cuda_device):
+    """Queries behind the last sequence's: the others' results as without them, their rows as they were."""
+    b = Batch(lens, n_new, hkv, hq, seed=26)
+    host, cache = b.cache8()
+    q = torch.randn(b.T, b.hq, 128, generator=b.gen).bfloat16()
+    sel, cnt = selection(b, k)
+    pad = 5
+    more = lambda t: torch.cat([t, t[:1].expand(pad, *t.shape[1:])]).contiguous()  # noqa: E731
+    queries = dsa.QueryBatch(b.queries.cu_q, more(b.pos).cuda())
+    for call, ws in ((dsa.sparse_attn_decode_fp8, True), (dsa.sparse_attn_prefill_fp8, False)):
+        want = call(cache, b.seqs, b.queries, q.cuda(), sel.cuda(), cnt.cuda())
+        out = torch.full((b.T + pad, b.hq, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((b.T + pad, b.hq), 7.0, device="cuda")
+        kw = dict(workspace=torch.zeros(dsa.decode_workspace_size(b.T + pad, b.hq, b.hkv, k), dtype=torch.uint8,
+                                        device="cuda")) if ws else {}
+        for _ in range(2):   # the second time on the workspace that the first one leaves
+            call(cache, b.seqs, queries, more(q).cuda(), more(sel).cuda(), more(cnt).cuda(), out=out, lse=lse,
+                 dev_err=b.err, **kw)
+            assert int(b.err) == 0
+            assert bool((out[b.T:] == 7).all()) and bool((lse[b.T:] == 7).all())
+            # the padding may change how a pair is split, and with it the running maxima that the
+            # weights are rounded against: two results differ by their roundings to bf16 and by
+            # 2 * 2^-11 of the weighted |v|, which is at most 448 * 2^-5 here; lse by two fp32 sums
+            # of at most 3000 terms
+            d = (out[:b.T].float() - want[0].float()).abs()
+            assert bool((d <= want[0].float().abs() * 2 * BF16_HALF + 2 * 2.0 ** -11 * 448 * 2.0 ** -5).all())
+            assert bool(((lse[:b.T] - want[1]).abs() <= 2 * 3008 * 2.0 ** -24).all())
+
+
 def test_attention_fp8_value_ranges(cuda_device):
     """Scales far apart between tiles, queries from 2^-90 to 2^60, a zero query, large and
     negative logits: within the tolerances of the same definition."""
