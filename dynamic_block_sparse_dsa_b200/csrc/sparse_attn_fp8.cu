@@ -32,8 +32,8 @@
 // tokens 2c, 2c+1, 2c+8 and 2c+9 of the column's dim, again the k indexes of one
 // mma (of the weights as the 16-bit transpose leaves them).
 //
-// Feeding.  Every warp is its own producer: it holds a ring of kSlots 8-KiB
-// slots for K and V tiles in turn and issues the TMA box of its next tile as
+// Feeding.  Every warp is its own producer: it holds kSlots 8-KiB slots, one
+// for K tiles and one for V tiles, and issues the TMA box of its next tile as
 // soon as it has read a slot.  Nothing is handed from warp to warp, so a tile
 // costs no queue words, fences or polls.  (A producer warp for the whole CTA,
 // as over the bf16 cache, needed about 600 cycles a tile here, with no
@@ -55,7 +55,7 @@
 // takes 2.40 ms: 680 instructions a tile, of them 256 conversions at two cycles
 // each, keep the ALU pipe 55 % and the tensor pipe 41 % busy; the gather alone
 // takes 1.67 ms (20 TB/s).  Decode reads its tiles once: 64 contexts of 8K, 135
-// MB, take 26.5 us (5.1 TB/s, 0.78 of the copy bandwidth) and 25.1 us without the
+// MB, take 26.7 us (5.1 TB/s, 0.77 of the copy bandwidth) and 25.1 us without the
 // arithmetic.
 #include "dsa_kernels.h"
 #include "dsa_tma.cuh"
