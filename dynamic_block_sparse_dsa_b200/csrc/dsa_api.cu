@@ -64,15 +64,28 @@ int sm_count() {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// decode workspace: [split counters int32 T*Hkv][partials f32 2*kAttnMaxCtas*G*kAttnPartStride]
+// decode workspace: [split counters int32][partials f32 2*kAttnMaxCtas*G*kAttnPartStride].
+// The counters have to read zero when a call starts, the partials are left as
+// the call wrote them: so both lie at the same place for every batch size and
+// group, and no call's partials are where a later call counts.  The counters
+// are those of the pairs that can be split, a fixed number.  The size is a
+// counter for each of the batch's pairs and 512 partial states, never less than
+// what is used (static_assert: the last kPartSpare states hold the counters).
+constexpr int kPartStates = 512, kPartSpare = kPartStates - 2 * kAttnMaxCtas;
+constexpr size_t kSplitCounterBytes = (size_t)kAttnSplitPairs * kAttnMaxCtas * sizeof(int32_t);
+static_assert(kSplitCounterBytes % 256 == 0 &&
+                  kSplitCounterBytes <= (size_t)kPartSpare * kAttnPartStride * sizeof(float),
+              "the workspace holds the split counters in front of the partial states");
 struct DecodeLayout {
     size_t counters, part, total;
 };
 DecodeLayout decode_layout(int total_q, int hq, int hkv) {
     DecodeLayout L;
     L.counters = 0;
-    L.part = align_up((size_t)total_q * hkv * sizeof(int32_t), 256);
-    L.total = align_up(L.part + (size_t)2 * kAttnMaxCtas * (hq / hkv) * kAttnPartStride * sizeof(float), 256);
+    L.part = kSplitCounterBytes;
+    L.total = align_up(align_up((size_t)total_q * hkv * sizeof(int32_t), 256) +
+                           (size_t)kPartStates * (hq / hkv) * kAttnPartStride * sizeof(float),
+                       256);
     return L;
 }
 
@@ -124,7 +137,7 @@ void attn_schedule(AttnArgs &a, bool allow_split, bool allow_cluster = false) {
     }
     // whole (query, KV head) pairs per CTA when there are plenty of them (or
     // when no workspace is available); otherwise split pairs across CTAs
-    a.pair_aligned = (!allow_split || pairs >= 16 * C) ? 1 : 0;
+    a.pair_aligned = (!allow_split || pairs >= kAttnSplitPairs * C) ? 1 : 0;
     const long long items = a.pair_aligned ? pairs : a.total_units;
     if (C > items) C = items;
     // a pair may be split over at most ~60 CTAs (the kernel merges <= 63 partials)

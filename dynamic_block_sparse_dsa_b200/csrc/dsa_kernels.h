@@ -184,7 +184,7 @@ struct AttnArgs {
     // `splits` CTAs, each taking an equal part of the pair's tiles
     int warps, warp_rounds, team, splits;   // warps per CTA
     float *part;             // [2*C][group][kAttnPartStride] partial (o[128], m, l) of split pairs
-    int32_t *counters;       // [T*Hkv] units merged so far per split pair
+    int32_t *counters;       // [split pair] units merged so far (zero between calls)
     int32_t *dev_err;
 };
 
@@ -237,8 +237,11 @@ cudaError_t launch_decode_fused(const AttnArgs &a, const FusedArgs &f, cudaStrea
 int check_decode_attn_args(const dsa_kv_cache *cache, const dsa_seqs *seqs, const dsa_queries *queries,
                            const void *q, int32_t num_q_heads, const int32_t *sel, const int32_t *cnt,
                            int32_t k_max, float sm_scale, void *out, float *lse);
-// largest grid the attention kernel uses (sizes the partial-state workspace)
-constexpr int kAttnMaxCtas = 256;
+// largest grid the attention kernels use
+constexpr int kAttnMaxCtas = 224;
+// pairs that a decode call can split over CTAs: the bf16 kernel splits batches of
+// fewer than kAttnSplitPairs pairs per CTA, the 8-bit kernel of fewer than one per two
+constexpr int kAttnSplitPairs = 16;
 // warps per CTA of the E4M3 attention kernel: 8, or 12 (168 registers a thread)
 // for groups of <= 8 heads with a pair for every warp
 constexpr int kFp8Warps = 8, kFp8ManyWarps = 12;

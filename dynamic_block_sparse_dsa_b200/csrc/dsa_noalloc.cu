@@ -70,10 +70,9 @@ extern "C" int dsa_sparse_attn_decode_noalloc(const dsa_kv_cache *cache, const d
         dsa_sparse_attn_decode_workspace_size(queries->total_q, num_q_heads, cache->num_kv_heads, k_max);
     if (need == 0) return DSA_ERR_INVALID_ARG;
     if (need > kScratchBytes) return DSA_ERR_WORKSPACE;   // problem too large for the fixed scratch
-    // the decode workspace starts with one int32 split counter per (query, KV
-    // head); they must read zero when the kernel starts
-    const size_t counter_bytes = (size_t)queries->total_q * cache->num_kv_heads * sizeof(int32_t);
-    if (counter_bytes > need) return DSA_ERR_INVALID_ARG;
+    // the decode workspace starts with the counters of the pairs that can be
+    // split; they must read zero when the kernel starts
+    constexpr size_t counter_bytes = (size_t)dsa::kAttnSplitPairs * dsa::kAttnMaxCtas * sizeof(int32_t);
     void *scratch = nullptr;
     rc = scratch_address(&scratch);
     if (rc != DSA_OK) return rc;

@@ -366,9 +366,11 @@ int dsa_select_blocks_append(const dsa_kv_cache *cache, const dsa_seqs *seqs, co
  * (through the workspace, or, when the batch has between a quarter and a half
  * as many pairs as the GPU has SMs, inside a 2-CTA cluster through
  * distributed shared memory); it needs a workspace of dsa_sparse_attn_decode_workspace_size() bytes (a
- * 4-byte counter per (query, KV head) pair plus room for two partial states
- * per CTA), zero-filled before its first use (each call leaves it zeroed
- * again).  The prefill entry keeps every pair
+ * 4-byte counter per (query, KV head) pair plus room for 512 partial states),
+ * zero-filled before its first use.  Each call leaves the counters at zero
+ * again, at a place that does not depend on the call: a workspace that is
+ * large enough serves calls of any batch size, group and cache type, one after
+ * the other.  The prefill entry keeps every pair
  * inside one CTA and needs no workspace.
  * Device errors: DSA_DEV_ERR_SEL, DSA_DEV_ERR_PAGE (that block is skipped).
  */

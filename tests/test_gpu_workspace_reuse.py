@@ -1,0 +1,60 @@
+"""One workspace through calls of different batches: zero-filled once, it serves
+every later call, whatever the batch size, the heads per KV head and (for the
+attention) the cache's type.  Each call's results are the bits of the same call
+on a fresh workspace; the kernels merge in a fixed order."""
+import pytest
+import torch
+
+import dynamic_block_sparse_dsa_b200 as dsa
+
+from test_gpu_rope_fp8 import Batch, selection
+
+pytestmark = pytest.mark.gpu
+
+
+def _decode_call(T, hkv, group, k, fp8, seed):
+    """(call(workspace) -> (out, lse), workspace size) of a decode batch of T contexts."""
+    b = Batch(tuple(1500 + 61 * i for i in range(T)), (1,) * T, hkv, hkv * group, seed=seed)
+    cache = (b.cache8() if fp8 else b.cache16())[1]
+    q = torch.randn(T, hkv * group, 128, generator=b.gen).bfloat16().cuda()
+    sel, cnt = selection(b, k)
+    sel, cnt = sel.cuda(), cnt.cuda()
+    fn = dsa.sparse_attn_decode_fp8 if fp8 else dsa.sparse_attn_decode
+
+    def call(ws):
+        out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+        fn(cache, b.seqs, b.queries, q, sel, cnt, out=out, lse=lse, workspace=ws, dev_err=b.err)
+        assert int(b.err) == 0
+        return out, lse
+
+    return call, dsa.decode_workspace_size(T, hkv * group, hkv, k)
+
+
+# batches of 2 to 320 pairs (split over CTAs below half as many pairs as SMs in the 8-bit kernel,
+# at any unaligned boundary in the bf16 one), growing, shrinking and growing again
+ORDERS = {
+    "fp8": [(8, 8, 8, True), (9, 8, 8, True), (8, 8, 8, True), (9, 8, 8, True)],
+    "bf16": [(20, 8, 8, False), (40, 8, 8, False), (20, 8, 8, False), (40, 8, 8, False)],
+    "mixed": [(20, 8, 4, False), (9, 8, 4, True), (2, 1, 4, True), (40, 8, 4, False), (9, 8, 4, True), (3, 1, 4, False),
+              (40, 8, 4, False)],
+    "groups": [(4, 2, 16, True), (9, 8, 1, True), (40, 8, 1, False), (4, 2, 16, False), (9, 8, 8, True), (40, 8, 4, False),
+               (9, 8, 1, True)],
+}
+
+
+@pytest.mark.parametrize("order", sorted(ORDERS))
+def test_decode_workspace_serves_batches_of_any_size(order, cuda_device):
+    calls, need = {}, 0
+    for i, key in enumerate(ORDERS[order]):
+        if key not in calls:
+            T, hkv, group, fp8 = key
+            call, size = _decode_call(T, hkv, group, 16, fp8, seed=70 + i)
+            want = call(torch.zeros(size, dtype=torch.uint8, device="cuda"))
+            assert not bool((want[0] == 7).all(-1).any())      # every row written
+            calls[key] = call, want
+            need = max(need, size)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for n, key in enumerate(ORDERS[order]):
+        call, want = calls[key]
+        out, lse = call(ws)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), (order, n, key)
