@@ -89,17 +89,11 @@ DecodeLayout decode_layout(int total_q, int hq, int hkv) {
     return L;
 }
 
-// select workspace: [counters int32 T][candidate keys u64 T*kSelMaxChunks*(kSelMaxK-1)]
-struct SelectLayout {
-    size_t counters, cand, total;
-};
-SelectLayout select_layout(int total_q) {
-    SelectLayout L;
-    L.counters = 0;
-    L.cand = align_up((size_t)total_q * sizeof(int32_t), 256);
-    L.total = align_up(L.cand + (size_t)total_q * kSelMaxChunks * (kSelMaxK - 1) * sizeof(unsigned long long), 256);
-    return L;
-}
+// select workspace: a record per query, [candidate keys u64 kSelMaxChunks*(kSelMaxK-1)][counter].
+// A query's counter, which has to read zero when a call starts, lies at a place
+// that does not depend on the batch: the candidates that a smaller batch left
+// are not where a larger one counts.
+size_t select_workspace_bytes(int total_q) { return align_up((size_t)total_q * kSelRecord * sizeof(unsigned long long), 256); }
 
 // single-launch decode workspace: [header 256 B][sel_count T][flags T]
 // [split counters T*Hkv][candidates kAttnMaxCtas*2*(kSelMaxK-1) u64][partials]
@@ -538,7 +532,7 @@ int dsa_topk_blocks_i64(const dsa_seqs *seqs, const dsa_queries *queries, const 
 
 size_t dsa_select_blocks_workspace_size(int32_t total_q) {
     if (total_q <= 0) return 0;
-    return select_layout(total_q).total;
+    return select_workspace_bytes(total_q);
 }
 
 int dsa_select_blocks(const dsa_kv_cache *cache, const dsa_seqs *seqs, const dsa_queries *queries,
@@ -604,8 +598,8 @@ int select_common(const dsa_kv_cache *cache, const dsa_seqs *seqs, const dsa_que
     if (bound >= (1LL << 31)) return DSA_ERR_RANGE;
     if (queries->total_q == 0) return DSA_OK;
     if (!q_idx || !w || !k_per_seq || !sel || !cnt || !aligned16(q_idx)) return DSA_ERR_INVALID_ARG;
-    const SelectLayout L = select_layout(queries->total_q);
-    if (!workspace || !aligned16(workspace) || workspace_bytes < L.total) return DSA_ERR_WORKSPACE;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < select_workspace_bytes(queries->total_q))
+        return DSA_ERR_WORKSPACE;
     SelectArgs a{};
     a.block_shift = block_shift_of(cache->block_size);
     a.kc_pool = cache->kc_pool;
@@ -624,9 +618,7 @@ int select_common(const dsa_kv_cache *cache, const dsa_seqs *seqs, const dsa_que
     a.k_max = k_max;
     a.sel = sel;
     a.cnt = cnt;
-    char *ws = static_cast<char *>(workspace);
-    a.counters = reinterpret_cast<int32_t *>(ws + L.counters);
-    a.cand = reinterpret_cast<unsigned long long *>(ws + L.cand);
+    a.records = static_cast<unsigned long long *>(workspace);
     a.dev_err = dev_err;
     a.cu_new = app ? app->cu_new : nullptr;
     if (app) a.app = *app;

@@ -107,6 +107,8 @@ struct TopkArgs {
 // fused score + Top-K (decode-oriented): candidate workspace layout
 constexpr int kSelMaxChunks = 32;   // chunks per query
 constexpr int kSelMaxK = 64;        // largest k_max of the fused path
+// 8-byte words of a query's workspace record: its chunks' keys, then its counter
+constexpr int kSelRecord = kSelMaxChunks * (kSelMaxK - 1) + 1;
 struct SelectArgs {
     const int8_t *kc_pool;
     int num_pages;
@@ -125,8 +127,9 @@ struct SelectArgs {
     int k_max;
     int32_t *sel;            // [T][k_max]
     int32_t *cnt;            // [T]
-    unsigned long long *cand;   // [T][kSelMaxChunks][kSelMaxK-1] 64-bit selection keys, sorted descending
-    int32_t *counters;       // [T] chunk CTAs done per query
+    // [T] records: [kSelMaxChunks][kSelMaxK-1] 64-bit selection keys, sorted descending, and a
+    // word with the number of chunk CTAs done (zero between calls)
+    unsigned long long *records;
     int32_t *dev_err;
     // append ordered after this selection (dsa_select_blocks_append): a
     // query whose sequence appends a block before its own block is refused

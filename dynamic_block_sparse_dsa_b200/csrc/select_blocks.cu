@@ -233,8 +233,11 @@ __global__ void __launch_bounds__(kSelThreads, G >= 2 ? 3 : 2) select_blocks_ker
         cta_merge_top64<kSelWarps>(acc, s_lists);   // sorted, in warp 0
     }
     bool from_ids = kChunkRadix;   // the winners' ids are in s_ids (else sorted in warp 0's acc)
+    // the query's workspace record
+    key64 *query_cand = a.records + (size_t)t * kSelRecord;
+    int32_t *query_count = reinterpret_cast<int32_t *>(query_cand + kSelRecord - 1);
     if (n_chunks > 1) {
-        key64 *cand = a.cand + ((size_t)t * kSelMaxChunks + c) * (kSelMaxK - 1);
+        key64 *cand = query_cand + c * (kSelMaxK - 1);
         if constexpr (kChunkRadix) {
             // in any order; slots past the chunk's winners are zeroed
             const int n_win = min(n_real, kk);
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(kSelThreads, G >= 2 ? 3 : 2) select_blocks_ker
         // every list before the loads below
         __syncthreads();
         if (tid == 0) {
-            const int old = atomic_add_acq_rel_gpu(a.counters + t, 1);
+            const int old = atomic_add_acq_rel_gpu(query_count, 1);
             s_last = (old == n_chunks - 1);
         }
         __syncthreads();
@@ -265,8 +268,7 @@ __global__ void __launch_bounds__(kSelThreads, G >= 2 ? 3 : 2) select_blocks_ker
             for (int j = 0; j < kLoad; ++j) {   // every load in flight before the selection
                 const int e = tid + j * kSelThreads;
                 const int ci = e / kk, ei = e - ci * kk;
-                lk[j] = e < n_slots ? __ldcg(a.cand + ((size_t)t * kSelMaxChunks + ci) * (kSelMaxK - 1) + ei)
-                                    : 0ull;
+                lk[j] = e < n_slots ? __ldcg(query_cand + ci * (kSelMaxK - 1) + ei) : 0ull;
             }
             cta_radix_threshold<kSelThreads, kLoad>(lk, (uint32_t)kk, s_rx, prefix, mask);
 #pragma unroll
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kSelThreads, G >= 2 ? 3 : 2) select_blocks_ker
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {   // every load in flight before the first merge
                 const int ci = warp + k * kSelWarps;
-                const key64 *src = a.cand + ((size_t)t * kSelMaxChunks + ci) * (kSelMaxK - 1);
+                const key64 *src = query_cand + ci * (kSelMaxK - 1);
                 const bool in = ci < n_chunks;
                 lists[k][0] = in && lane < kk ? __ldcg(src + lane) : 0ull;
                 lists[k][1] = in && 32 + lane < kk ? __ldcg(src + 32 + lane) : 0ull;
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(kSelThreads, G >= 2 ? 3 : 2) select_blocks_ker
         if (lane == 0) {
             out[km] = own;              // the own block: the largest visible id, last in order
             a.cnt[t] = km + 1;
-            a.counters[t] = 0;          // ready for the next call
+            if (n_chunks > 1) *query_count = 0;   // ready for the next call
         }
         for (int i = km + 1 + lane; i < a.k_max; i += 32) out[i] = -1;
         // the attention that follows looks these blocks' pages up first: warm

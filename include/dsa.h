@@ -318,7 +318,9 @@ int dsa_topk_blocks_i64(const dsa_seqs *seqs, const dsa_queries *queries, const 
  * query's visible blocks are scored in chunks by separate CTAs that keep their
  * local Top-(K-1); the last CTA of the query merges them.  Needs a workspace
  * of dsa_select_blocks_workspace_size(total_q) bytes, zero-filled before its
- * first use (each call leaves its counters at zero again).
+ * first use.  Each call leaves its counters at zero again, at places that do
+ * not depend on the batch: a workspace that is large enough serves batches of
+ * any size, one after the other.
  * Device errors: DSA_DEV_ERR_PAGE, DSA_DEV_ERR_POS, DSA_DEV_ERR_K.
  */
 size_t dsa_select_blocks_workspace_size(int32_t total_q);

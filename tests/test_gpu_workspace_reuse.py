@@ -58,3 +58,42 @@ def test_decode_workspace_serves_batches_of_any_size(order, cuda_device):
         call, want = calls[key]
         out, lse = call(ws)
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), (order, n, key)
+
+
+def _select_case(T, blocks=20000, seed=5):
+    """A decode batch whose contexts share their pages (only the coarse keys are read): several
+    chunks of candidates per query."""
+    g = torch.Generator().manual_seed(seed + T)
+    pages = blocks
+    pool = torch.zeros((pages, 64, 1, 128), dtype=torch.uint8, device="cuda")
+    scale = torch.ones((pages, 1, 1), device="cuda")
+    kc = torch.randint(-127, 128, (pages, 64), generator=torch.Generator().manual_seed(seed), dtype=torch.int8).cuda()
+    cache = dsa.PagedKVCacheFP8(pool, pool, kc, scale, scale)
+    table = torch.randperm(pages, generator=g).int()[None].expand(T, pages).contiguous().cuda()
+    lens = torch.full((T,), blocks * 64, dtype=torch.int32).cuda()
+    cu = torch.arange(T + 1, dtype=torch.int32).cuda()
+    q_idx = torch.randint(-127, 128, (T, 16, 64), generator=g, dtype=torch.int8).cuda()
+    w = torch.randint(0, 17, (T, 16), generator=g, dtype=torch.int32).cuda()
+    kps = torch.full((T,), 64, dtype=torch.int32).cuda()
+    seqs, queries = dsa.SeqBatch(table, lens), dsa.QueryBatch(cu, lens - 1)
+
+    def call(ws):
+        sel = torch.full((T, 64), -9, dtype=torch.int32, device="cuda")
+        cnt = torch.full((T,), -9, dtype=torch.int32, device="cuda")
+        return dsa.select_blocks(cache, seqs, queries, q_idx, w, kps, 64, sel=sel, cnt=cnt, workspace=ws)
+    return call
+
+
+def test_select_workspace_serves_batches_of_any_size(cuda_device):
+    sizes = (8, 100, 3, 100, 40, 8, 100)
+    calls = {}
+    for T in set(sizes):
+        call = _select_case(T)
+        want = call(torch.zeros(dsa.select_workspace_size(T), dtype=torch.uint8, device="cuda"))
+        assert bool((want[1] == 64).all())
+        calls[T] = call, want
+    ws = torch.zeros(dsa.select_workspace_size(max(sizes)), dtype=torch.uint8, device="cuda")
+    for n, T in enumerate(sizes):
+        call, want = calls[T]
+        sel, cnt = call(ws)
+        assert torch.equal(sel, want[0]) and torch.equal(cnt, want[1]), (n, T)
