@@ -95,18 +95,20 @@ DecodeLayout decode_layout(int total_q, int hq, int hkv) {
 // are not where a larger one counts.
 size_t select_workspace_bytes(int total_q) { return align_up((size_t)total_q * kSelRecord * sizeof(unsigned long long), 256); }
 
-// single-launch decode workspace: [header 256 B][sel_count T][flags T]
-// [split counters T*Hkv][candidates kAttnMaxCtas*2*(kSelMaxK-1) u64][partials]
+// single-launch decode workspace: [header 256 B][sel_count][flags][split counters]
+// [candidates kAttnMaxCtas*2*(kSelMaxK-1) u64][partials].  What a call finds as
+// the one before it left it (header, counts, flags, counters) has a fixed place,
+// so that batches of any size can follow one another on one workspace.
 struct FusedLayout {
     size_t hdr, sel_count, flags, counters, cand, part, total;
 };
-FusedLayout fused_layout(int total_q, int hq, int hkv) {
+FusedLayout fused_layout(int hq, int hkv) {
     FusedLayout L;
     L.hdr = 0;
     L.sel_count = 256;
-    L.flags = align_up(L.sel_count + (size_t)total_q * 4, 256);
-    L.counters = align_up(L.flags + (size_t)total_q * 4, 256);
-    L.cand = align_up(L.counters + (size_t)total_q * hkv * 4, 256);
+    L.flags = L.sel_count + align_up((size_t)kFusedMaxQ * 4, 256);
+    L.counters = L.flags + align_up((size_t)kFusedMaxQ * 4, 256);
+    L.cand = L.counters + kSplitCounterBytes;
     L.part = align_up(L.cand + (size_t)kAttnMaxCtas * 2 * (kSelMaxK - 1) * sizeof(unsigned long long), 256);
     L.total = align_up(L.part + (size_t)2 * kAttnMaxCtas * (hq / hkv) * kAttnPartStride * sizeof(float), 256);
     return L;
@@ -656,7 +658,7 @@ size_t dsa_decode_fused_workspace_size(int32_t total_q, int32_t num_q_heads, int
                                        int32_t k_max) {
     if (total_q <= 0 || num_q_heads < 1 || num_kv_heads < 1 || k_max < 1 || num_q_heads % num_kv_heads)
         return 0;
-    return fused_layout(total_q, num_q_heads, num_kv_heads).total;
+    return fused_layout(num_q_heads, num_kv_heads).total;
 }
 
 int dsa_decode_fused(const dsa_kv_cache *cache, const dsa_seqs *seqs, const dsa_queries *queries,
@@ -680,7 +682,7 @@ int dsa_decode_fused(const dsa_kv_cache *cache, const dsa_seqs *seqs, const dsa_
     }
     if (queries->total_q == 0) return DSA_OK;
     if (!q_idx || !w || !k_per_seq || !aligned16(q_idx)) return DSA_ERR_INVALID_ARG;
-    const FusedLayout L = fused_layout(queries->total_q, num_q_heads, cache->num_kv_heads);
+    const FusedLayout L = fused_layout(num_q_heads, cache->num_kv_heads);
     if (!workspace || !aligned16(workspace) || workspace_bytes < L.total) return DSA_ERR_WORKSPACE;
     char *ws = static_cast<char *>(workspace);
     a.counters = reinterpret_cast<int32_t *>(ws + L.counters);

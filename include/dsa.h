@@ -426,8 +426,9 @@ int dsa_sparse_attn_prefill_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *s
  *    DSA_DEV_ERR_POS and cnt 0.  With total_new == 0 nothing is appended.
  *  - total_q <= 1024, k_max <= 64, num_idx_heads <= 16.
  *  - Needs a workspace of dsa_decode_fused_workspace_size() bytes, zero-filled
- *    before its first use; each call leaves it ready for the next (it keeps a
- *    call counter, so calls that share one workspace must not overlap).
+ *    before its first use; each call leaves it ready for the next, of whatever
+ *    batch size (it keeps a call counter, so calls that share one workspace
+ *    must not overlap).
  *  - Every CTA of the grid must be resident at once (a cooperative launch):
  *    the call fails with DSA_ERR_CUDA if the GPU cannot give it one CTA per
  *    SM.  Waits between phases are bounded (DSA_DEV_ERR_WAIT on timeout).

@@ -97,3 +97,38 @@ def test_select_workspace_serves_batches_of_any_size(cuda_device):
         call, want = calls[T]
         sel, cnt = call(ws)
         assert torch.equal(sel, want[0]) and torch.equal(cnt, want[1]), (n, T)
+
+
+def _fused_call(T, hkv, group, seed):
+    """A decode batch through the single-launch step; the appended rows are the same every time."""
+    b = Batch(tuple(5000 + 777 * i for i in range(T)), (1,) * T, hkv, hkv * group, seed=seed)
+    cache = b.cache16()[1]
+    q_idx = torch.randint(-127, 128, (T, 16, 64), generator=b.gen, dtype=torch.int8).cuda()
+    w = torch.randint(0, 17, (T, 16), generator=b.gen, dtype=torch.int32).cuda()
+    kps = torch.full((T,), 12, dtype=torch.int32).cuda()
+    kc = b.kc.cuda()
+
+    def call(ws):
+        got = [torch.full((T, 12), -9, dtype=torch.int32, device="cuda"), torch.full((T,), -9, dtype=torch.int32, device="cuda"),
+               torch.full_like(b.dq, 7.0), torch.full(b.dq.shape[:2], 7.0, device="cuda")]
+        dsa.decode_fused(cache, b.seqs, b.queries, b.queries.cu_q, b.dk, b.dv, kc, q_idx, w, kps, 12, b.dq, sel=got[0],
+                         cnt=got[1], out=got[2], lse=got[3], workspace=ws, dev_err=b.err)
+        assert int(b.err) == 0
+        return got
+
+    return call, dsa.decode_fused_workspace_size(T, hkv * group, hkv, 12)
+
+
+def test_fused_decode_workspace_serves_batches_of_any_size(cuda_device):
+    order = [(3, 2, 4), (40, 2, 4), (3, 2, 4), (2, 1, 16), (40, 2, 4), (17, 8, 2), (2, 1, 16), (40, 2, 4)]
+    calls, need = {}, 0
+    for i, key in enumerate(order):
+        if key not in calls:
+            call, size = _fused_call(*key, seed=75 + i)
+            calls[key] = call, call(torch.zeros(size, dtype=torch.uint8, device="cuda"))
+            need = max(need, size)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for n, key in enumerate(order):
+        call, want = calls[key]
+        for got, w in zip(call(ws), want):
+            assert torch.equal(got, w), (n, key)
