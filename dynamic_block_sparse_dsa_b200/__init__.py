@@ -101,6 +101,22 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+def _workspace(size: int, dev, stream) -> torch.Tensor:
+    """A workspace for a call on ``stream``, its zero fill ordered before that call."""
+    with _on(stream):
+        return torch.zeros(size, dtype=torch.uint8, device=dev)
+
+
+def _sel_out(total_q: int, k_max: int, dev, sel, cnt, stream):
+    if sel is None or cnt is None:
+        with _on(stream):
+            if sel is None:
+                sel = torch.empty((total_q, k_max), dtype=torch.int32, device=dev)
+            if cnt is None:
+                cnt = torch.empty((total_q,), dtype=torch.int32, device=dev)
+    return sel, cnt
+
+
 @dataclass
 class PagedKVCache:
     """Block-paged pools: k/v bf16 [num_pages][block_size][num_kv_heads][128], kc int8
@@ -380,8 +396,8 @@ def index_score(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, q_idx:
     _expect(q_idx, torch.int8, "q_idx")
     _expect(w, torch.int32, "w")
     if scores is None:
-        scores = torch.empty((queries.total_q, seqs.block_table.shape[1]), dtype=torch.int32,
-                             device=q_idx.device)
+        with _on(stream):
+            scores = torch.empty((queries.total_q, seqs.block_table.shape[1]), dtype=torch.int32, device=q_idx.device)
     c, s, q = cache.index_ctype(), seqs.ctype(), queries.ctype()
     _lib.check("dsa_index_score", lib.dsa_index_score(
         ctypes.byref(c), ctypes.byref(s), ctypes.byref(q), _ptr(q_idx), _ptr(w), q_idx.shape[1],
@@ -395,11 +411,7 @@ def topk_blocks(seqs: SeqBatch, queries: QueryBatch, scores: torch.Tensor, k_per
     """(sel int32 [total_q][k_max] ascending logical ids, -1 padded; cnt int32 [total_q]).
     ``block_size`` is the tokens per block of the cache the scores came from."""
     lib = load()
-    dev = scores.device
-    if sel is None:
-        sel = torch.empty((queries.total_q, k_max), dtype=torch.int32, device=dev)
-    if cnt is None:
-        cnt = torch.empty((queries.total_q,), dtype=torch.int32, device=dev)
+    sel, cnt = _sel_out(queries.total_q, k_max, scores.device, sel, cnt, stream)
     s, q = seqs.ctype(), queries.ctype()
     _lib.check("dsa_topk_blocks", lib.dsa_topk_blocks(
         ctypes.byref(s), ctypes.byref(q), _ptr(scores), _ptr(k_per_seq), int(k_max), int(block_size), _ptr(sel),
@@ -414,7 +426,8 @@ def index_score_i64(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, q_
     _expect(q_idx, torch.int8, "q_idx")
     _expect(w, torch.int32, "w")
     if scores is None:
-        scores = torch.empty((queries.total_q, seqs.block_table.shape[1]), dtype=torch.int64, device=q_idx.device)
+        with _on(stream):
+            scores = torch.empty((queries.total_q, seqs.block_table.shape[1]), dtype=torch.int64, device=q_idx.device)
     c, s, q = cache.index_ctype(), seqs.ctype(), queries.ctype()
     _lib.check("dsa_index_score_i64", lib.dsa_index_score_i64(
         ctypes.byref(c), ctypes.byref(s), ctypes.byref(q), _ptr(q_idx), _ptr(w), q_idx.shape[1], _ptr(scores),
@@ -433,8 +446,8 @@ def index_score_fp8(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, q_
     _expect(q_idx_e4m3, torch.uint8, "q_idx_e4m3")
     _expect(w, torch.int32, "w")
     if scores is None:
-        scores = torch.empty((queries.total_q, seqs.block_table.shape[1]), dtype=torch.int64,
-                             device=q_idx_e4m3.device)
+        with _on(stream):
+            scores = torch.empty((queries.total_q, seqs.block_table.shape[1]), dtype=torch.int64, device=q_idx_e4m3.device)
     c, s, q = cache.index_ctype(), seqs.ctype(), queries.ctype()
     _lib.check("dsa_index_score_fp8", lib.dsa_index_score_fp8(
         ctypes.byref(c), ctypes.byref(s), ctypes.byref(q), _ptr(q_idx_e4m3), _ptr(w), q_idx_e4m3.shape[1],
@@ -448,11 +461,7 @@ def topk_blocks_i64(seqs: SeqBatch, queries: QueryBatch, scores: torch.Tensor, k
     """topk_blocks over int64 scores (index_score_i64 / index_score_fp8)."""
     lib = load()
     _expect(scores, torch.int64, "scores")
-    dev = scores.device
-    if sel is None:
-        sel = torch.empty((queries.total_q, k_max), dtype=torch.int32, device=dev)
-    if cnt is None:
-        cnt = torch.empty((queries.total_q,), dtype=torch.int32, device=dev)
+    sel, cnt = _sel_out(queries.total_q, k_max, scores.device, sel, cnt, stream)
     s, q = seqs.ctype(), queries.ctype()
     _lib.check("dsa_topk_blocks_i64", lib.dsa_topk_blocks_i64(
         ctypes.byref(s), ctypes.byref(q), _ptr(scores), _ptr(k_per_seq), int(k_max), int(block_size), _ptr(sel),
@@ -473,14 +482,9 @@ def select_blocks(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, q_id
     lib = load()
     _expect(q_idx, torch.int8, "q_idx")
     _expect(w, torch.int32, "w")
-    dev = q_idx.device
-    T = queries.total_q
-    if sel is None:
-        sel = torch.empty((T, k_max), dtype=torch.int32, device=dev)
-    if cnt is None:
-        cnt = torch.empty((T,), dtype=torch.int32, device=dev)
+    sel, cnt = _sel_out(queries.total_q, k_max, q_idx.device, sel, cnt, stream)
     if workspace is None:
-        workspace = torch.zeros(select_workspace_size(T), dtype=torch.uint8, device=dev)
+        workspace = _workspace(select_workspace_size(queries.total_q), q_idx.device, stream)
     c, s, q = cache.index_ctype(), seqs.ctype(), queries.ctype()
     _lib.check("dsa_select_blocks", lib.dsa_select_blocks(
         ctypes.byref(c), ctypes.byref(s), ctypes.byref(q), _ptr(q_idx), _ptr(w), q_idx.shape[1], int(w_abs_max),
@@ -503,14 +507,9 @@ def select_blocks_append(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatc
     _expect(w, torch.int32, "w")
     _expect(k_new, torch.bfloat16, "k_new")
     _expect(v_new, torch.bfloat16, "v_new")
-    dev = q_idx.device
-    T = queries.total_q
-    if sel is None:
-        sel = torch.empty((T, k_max), dtype=torch.int32, device=dev)
-    if cnt is None:
-        cnt = torch.empty((T,), dtype=torch.int32, device=dev)
+    sel, cnt = _sel_out(queries.total_q, k_max, q_idx.device, sel, cnt, stream)
     if workspace is None:
-        workspace = torch.zeros(select_workspace_size(T), dtype=torch.uint8, device=dev)
+        workspace = _workspace(select_workspace_size(queries.total_q), q_idx.device, stream)
     c, s, q = cache.ctype(), seqs.ctype(), queries.ctype()
     _lib.check("dsa_select_blocks_append", lib.dsa_select_blocks_append(
         ctypes.byref(c), ctypes.byref(s), ctypes.byref(q), _ptr(cu_new), k_new.shape[0], _ptr(k_new), _ptr(v_new),
@@ -523,11 +522,13 @@ def decode_workspace_size(total_q: int, num_q_heads: int, num_kv_heads: int, k_m
     return int(load().dsa_sparse_attn_decode_workspace_size(total_q, num_q_heads, num_kv_heads, k_max))
 
 
-def _attn_out(q, out, lse):
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+def _attn_out(q, out, lse, stream):
+    if out is None or lse is None:
+        with _on(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if lse is None:
+                lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     return out, lse
 
 
@@ -540,10 +541,10 @@ def sparse_attn_decode(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch,
     lib = load()
     _expect(q, torch.bfloat16, "q")
     k_max = sel.shape[1]
-    out, lse = _attn_out(q, out, lse)
+    out, lse = _attn_out(q, out, lse, stream)
     if workspace is None:
-        workspace = torch.zeros(decode_workspace_size(queries.total_q, q.shape[1], cache.num_kv_heads, k_max),
-                                dtype=torch.uint8, device=q.device)
+        workspace = _workspace(decode_workspace_size(queries.total_q, q.shape[1], cache.num_kv_heads, k_max), q.device,
+                               stream)
     scale = 1.0 / math.sqrt(q.shape[2]) if sm_scale is None else float(sm_scale)
     c, s, qq = cache.ctype(), seqs.ctype(), queries.ctype()
     _lib.check("dsa_sparse_attn_decode", lib.dsa_sparse_attn_decode(
@@ -564,7 +565,7 @@ def sparse_attn_decode_noalloc(cache: PagedKVCache, seqs: SeqBatch, queries: Que
     here only when not given."""
     lib = load()
     _expect(q, torch.bfloat16, "q")
-    out, lse = _attn_out(q, out, lse)
+    out, lse = _attn_out(q, out, lse, stream)
     scale = 1.0 / math.sqrt(q.shape[2]) if sm_scale is None else float(sm_scale)
     c, s, qq = cache.ctype(), seqs.ctype(), queries.ctype()
     _lib.check("dsa_sparse_attn_decode_noalloc", lib.dsa_sparse_attn_decode_noalloc(
@@ -578,7 +579,7 @@ def sparse_attn_prefill(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch
                         out=None, lse=None, dev_err: Optional[torch.Tensor] = None, stream=None):
     lib = load()
     _expect(q, torch.bfloat16, "q")
-    out, lse = _attn_out(q, out, lse)
+    out, lse = _attn_out(q, out, lse, stream)
     scale = 1.0 / math.sqrt(q.shape[2]) if sm_scale is None else float(sm_scale)
     c, s, qq = cache.ctype(), seqs.ctype(), queries.ctype()
     _lib.check("dsa_sparse_attn_prefill", lib.dsa_sparse_attn_prefill(
@@ -599,9 +600,7 @@ def _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, stream
         raise ValueError(f"sel must be [{T}][k_max] and cnt [{T}]")
     if queries.cu_q.numel() != seqs.block_table.shape[0] + 1:
         raise ValueError("cu_q must have one entry more than there are sequences")
-    if out is None or lse is None:
-        with _on(stream):
-            out, lse = _attn_out(q, out, lse)
+    out, lse = _attn_out(q, out, lse, stream)
     rows = q.shape
     if out.shape != rows or lse.shape != rows[:2]:
         raise ValueError("out must have q's shape and lse its first two dimensions")
@@ -639,9 +638,8 @@ def sparse_attn_decode_fp8(cache: PagedKVCacheFP8, seqs: SeqBatch, queries: Quer
             return out, lse
     dev, out, lse, args = _attn_fp8_args(cache, seqs, queries, q, sel, cnt, sm_scale, out, lse, stream)
     if workspace is None:
-        with _on(stream):
-            workspace = torch.zeros(decode_workspace_size(queries.total_q, q.shape[1], cache.num_kv_heads,
-                                                          sel.shape[1]), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(decode_workspace_size(queries.total_q, q.shape[1], cache.num_kv_heads, sel.shape[1]),
+                               q.device, stream)
     rc = lib.dsa_sparse_attn_decode_fp8(
         *args, _at(workspace, workspace.dtype, dev, "workspace"), workspace.numel() * workspace.element_size(),
         None if dev_err is None else _at(dev_err, torch.int32, dev, "dev_err"), _raw_stream(stream, dev))
@@ -686,15 +684,11 @@ def decode_fused(cache: PagedKVCache, seqs: SeqBatch, queries: QueryBatch, cu_ne
     _expect(q, torch.bfloat16, "q")
     _expect(q_idx, torch.int8, "q_idx")
     _expect(w, torch.int32, "w")
-    T, dev = queries.total_q, q.device
-    if sel is None:
-        sel = torch.empty((T, k_max), dtype=torch.int32, device=dev)
-    if cnt is None:
-        cnt = torch.empty((T,), dtype=torch.int32, device=dev)
-    out, lse = _attn_out(q, out, lse)
+    sel, cnt = _sel_out(queries.total_q, k_max, q.device, sel, cnt, stream)
+    out, lse = _attn_out(q, out, lse, stream)
     if workspace is None:
-        workspace = torch.zeros(decode_fused_workspace_size(T, q.shape[1], cache.num_kv_heads, k_max),
-                                dtype=torch.uint8, device=dev)
+        workspace = _workspace(decode_fused_workspace_size(queries.total_q, q.shape[1], cache.num_kv_heads, k_max),
+                               q.device, stream)
     total_new = 0 if k_new is None else k_new.shape[0]
     if k_new is not None:
         _expect(k_new, torch.bfloat16, "k_new")
@@ -807,18 +801,22 @@ class PreparedStep:
                  stream=None, stager: Optional[Stager] = None, slot: int = 0, host_in=(), host_out=(),
                  **step_kwargs):
         global load
-        rec = _Recorder(_lib.load())
-        saved = load
-        load = lambda: rec   # noqa: E731 -- the binding's calls below go to the recorder
-        try:
-            self.bufs = step(cache, seqs, queries, bufs=bufs, **step_kwargs)
-        finally:
-            load = saved
-        self.calls = rec.calls
         if stager is not None:
             if not 0 <= slot < stager.num_slots:
                 raise ValueError(f"slot {slot} outside the stager's {stager.num_slots} slots")
             stream = stager.stream
+        rec = _Recorder(_lib.load())
+        saved, had = load, set(bufs or ())
+        load = lambda: rec   # noqa: E731 -- the binding's calls below go to the recorder
+        try:
+            self.bufs = step(cache, seqs, queries, bufs=bufs, stream=stream, **step_kwargs)
+        finally:
+            load = saved
+        self.calls = rec.calls
+        if any(t.is_cuda for n, t in self.bufs.items() if n not in had) and not torch.cuda.is_current_stream_capturing():
+            # new workspaces are zero before a call on any stream
+            (torch.cuda.current_stream() if stream is None else stream).synchronize()
+        if stager is not None:
             lib = _lib.load()
             self._stager = stager
             self._begin = (lib.dsa_stager_begin, (stager._h, slot, *_rotate(_regions(host_in, False))))
@@ -873,7 +871,8 @@ def step(cache, seqs: SeqBatch, queries: QueryBatch, *, k_new, v_new, kc_new, q,
     The overlapped append and the single-launch step take neither.
 
     ``bufs`` (optional, reused across calls) holds the scores / sel / cnt /
-    out / lse / workspace tensors; missing ones are allocated.  Returns bufs.
+    out / lse / workspace tensors; missing ones are allocated on the call's
+    stream.  Returns bufs.
     """
     b = {} if bufs is None else bufs
     fp8 = isinstance(cache, PagedKVCacheFP8)
@@ -883,20 +882,18 @@ def step(cache, seqs: SeqBatch, queries: QueryBatch, *, k_new, v_new, kc_new, q,
         raise ValueError("pos needs rope")
     T, dev = queries.total_q, q.device
     if "scores" not in b:
-        b["scores"] = torch.empty((T, seqs.block_table.shape[1]), dtype=torch.int32, device=dev)
-        b["sel"] = torch.empty((T, k_max), dtype=torch.int32, device=dev)
-        b["cnt"] = torch.empty((T,), dtype=torch.int32, device=dev)
-        b["out"] = torch.empty_like(q)
-        b["lse"] = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-        b["workspace"] = torch.zeros(decode_workspace_size(T, q.shape[1], cache.num_kv_heads, k_max),
-                                     dtype=torch.uint8, device=dev)
-        b["select_ws"] = torch.zeros(select_workspace_size(T), dtype=torch.uint8, device=dev)
+        with _on(stream):
+            b["scores"] = torch.empty((T, seqs.block_table.shape[1]), dtype=torch.int32, device=dev)
+        b["sel"], b["cnt"] = _sel_out(T, k_max, dev, None, None, stream)
+        b["out"], b["lse"] = _attn_out(q, None, None, stream)
+        b["workspace"] = _workspace(decode_workspace_size(T, q.shape[1], cache.num_kv_heads, k_max), dev, stream)
+        b["select_ws"] = _workspace(select_workspace_size(T), dev, stream)
     if fused_decode:
         if not decode:
             raise ValueError("fused_decode needs a decode batch")
         if "fused_ws" not in b:
-            b["fused_ws"] = torch.zeros(decode_fused_workspace_size(T, q.shape[1], cache.num_kv_heads, k_max),
-                                        dtype=torch.uint8, device=dev)
+            b["fused_ws"] = _workspace(decode_fused_workspace_size(T, q.shape[1], cache.num_kv_heads, k_max), dev,
+                                       stream)
         decode_fused(cache, seqs, queries, queries.cu_q, k_new, v_new, kc_new, q_idx, w, k_per_seq, k_max, q,
                      w_abs_max, sel=b["sel"], cnt=b["cnt"], out=b["out"], lse=b["lse"], workspace=b["fused_ws"],
                      dev_err=dev_err, stream=stream)
