@@ -10,11 +10,12 @@
 //     (x, y) -> (x cos - y sin, y cos + x sin) * scale.
 // At a million tokens p * inv_freq in fp32 is off by up to 0.06 rad, so the
 // angle is kept in turns as a 64-bit fraction: f = inv_freq / (2 pi) mod 1
-// times 2^64, and p * f mod 2^64 is the fraction of a turn, exact but for the
-// rounding of f (2^-53 of a turn per position).  Its upper 32 bits give the
-// nearest quarter turn and a remainder in [-pi/4, pi/4], whose sine and cosine
-// are Taylor sums (to x^9 and x^8: the next terms are below 2^-25 there).  The
-// rotation itself is fp32, rounded once to the stored type.
+// times 2^64, and p * f mod 2^64 is the fraction of a turn.  f is off by at most
+// 2^-63 (turns_q64), the fraction at any int32 position by 2^-32.  Its upper 32
+// bits give the nearest quarter turn and a remainder in [-pi/4, pi/4], rounded
+// to fp32 (2^-26 of a turn), whose sine and cosine are Taylor sums (to x^9 and
+// x^8: the next terms are below 2^-25 there).  The rotation itself is fp32,
+// rounded once to the stored type.
 //
 // E4M3 cache.  A tile is 64 tokens of a block; each (tile, KV head) has one
 // scale for K and one for V, a power of two when written here:
@@ -49,11 +50,16 @@ constexpr int kPairs = kHeadDim / 2;
 constexpr int kMinScaleExp = -100;
 constexpr int kMaxAxes = 4;
 
-// the fraction of a turn per position as a 64-bit fixed-point number
+// The fraction of a turn per position as a 64-bit fixed-point number.  1 / (2 pi)
+// is the sum of two doubles, and the product with the first is kept with its
+// rounding error: the product of one double alone is off by 2^-53 of its size,
+// which at inv_freq 100 and position 2^31 is 2.6e-6 of a turn.  The whole turns
+// drop out exactly (hi - rint(hi)); the two conversions cut off below 2^-64 each.
 __device__ __forceinline__ unsigned long long turns_q64(float inv_freq) {
-    double f = (double)inv_freq * 0.15915494309189535;   // 1 / (2 pi)
-    f -= floor(f);
-    return (unsigned long long)(f * 18446744073709551616.0);
+    constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
+    constexpr double kOne = 18446744073709551616.0;   // 2^64
+    const double x = inv_freq, hi = x * kHi, lo = fma(x, kHi, -hi) + x * kLo;
+    return (unsigned long long)((long long)((hi - rint(hi)) * kOne) + (long long)(lo * kOne));
 }
 
 // (cos, sin) of the angle at position p, times the rotation's scale

@@ -140,7 +140,8 @@ int dsa_kv_append(const dsa_kv_cache *cache, const dsa_seqs *seqs, const int32_t
  * attending.  Pair i of a row (i < rotary_dim / 2) at position p becomes
  *     (x cos a - y sin a, y cos a + x sin a) * scale,   a = p * inv_freq[i],
  * computed in fp32 from an angle that is exact to 2^-24 of a turn at any int32
- * position, and rounded once.  Dims from rotary_dim on are copied.
+ * position (for |inv_freq| <= 2^32), and rounded once.  Dims from rotary_dim on
+ * are copied.
  *   layout: DSA_ROPE_HALVES pairs dims (i, i + rotary_dim / 2), DSA_ROPE_PAIRS
  *           dims (2i, 2i + 1).
  *   rotary_dim: a multiple of 16, 16..128 (others are DSA_ERR_UNSUPPORTED).
