@@ -365,7 +365,9 @@ def kv_append_rope(cache: PagedKVCache, seqs: SeqBatch, cu_new: Optional[torch.T
     packed projection (only the tokens apart); ``q_out`` may be a contiguous
     ``q`` itself.  ``pos_new``/``pos_q`` are int32 [num_axes][tokens] positions,
     by default each token's place in its sequence.  ``k_new`` None: nothing
-    is appended, only the queries are rotated."""
+    is appended, only the queries are rotated.  The rows (k, v, q, coarse keys)
+    may come from any kernel before the call; the positions and the batch's
+    description not from one that lets its successors start early (include/dsa.h)."""
     if not isinstance(cache, PagedKVCache):
         raise TypeError("kv_append_rope appends to a PagedKVCache (kv_append_fp8 to a PagedKVCacheFP8)")
     return _append_rope("dsa_kv_append_rope", cache, seqs, cu_new, k_new, v_new, kc_new, rope, pos_new, queries, q,
@@ -381,7 +383,9 @@ def kv_append_fp8(cache: PagedKVCacheFP8, seqs: SeqBatch, cu_new: Optional[torch
     """kv_append_rope into the 8-bit cache, quantised on the way (``rope`` None:
     the keys are stored as they come).  Each (64-token tile, KV head) has one
     power-of-two scale for K and one for V, which grows when a new token needs
-    it; the tile's earlier codes are then rounded anew."""
+    it; the tile's earlier codes are then rounded anew.  As there, the rows may
+    come from any kernel before the call, the positions and the batch's
+    description not from one that lets its successors start early."""
     if not isinstance(cache, PagedKVCacheFP8):
         raise TypeError("kv_append_fp8 appends to a PagedKVCacheFP8")
     return _append_rope("dsa_kv_append_fp8", cache, seqs, cu_new, k_new, v_new, kc_new, rope, pos_new, queries, q,

@@ -47,6 +47,9 @@ namespace {
 constexpr int kThreads = 256, kSlots = kThreads / 8;   // eight threads (32 bytes of a row each) per row
 constexpr int kTileThreads = 2 * kThreads;             // E4M3 append: a row of a full tile per eight threads
 constexpr int kPairs = kHeadDim / 2;
+// CTAs per SM of the two kernels: with the SMs, the first wave, which may start
+// before the kernel ahead ends
+constexpr int kRopeCtas = 5, kTileCtas = 2, kSms = 148;
 constexpr int kMinScaleExp = -100;
 constexpr int kMaxAxes = 4;
 
@@ -192,11 +195,14 @@ __device__ __forceinline__ Place place_of(const KvAppendArgs &a, int i, uint32_t
 
 // the rotated query rows of one query and, in the bf16 cache, the K and V rows
 // of one new token: row r of the CTA's list is K head r, then V head, then
-// query head.  Loads of kBatch rows per thread are issued before the tables
-// (s_tab: K, q) are ready and before the wait for the kernels ahead.  kThreads
+// query head.  The rows may come from a kernel ahead and are read behind the wait
+// for it.  A CTA of the first wave (early) looks up the token's place and forms
+// the tables (s_tab: K, q) before that wait; the others, for which it is over,
+// have the rows' first loads (kBatch per thread) under way meanwhile.  (8 decode
+// tokens: 2.4 us early, 3.4 us not; 4096 tokens: 34.6 and 31.2 us.)  kThreads
 // threads numbered tid share it; all threads of the CTA call it.
 template <bool kKv>
-__device__ __forceinline__ void token_rows(const AppendRopeArgs &a, int i, int tid, RopeTab *s_tab) {
+__device__ __forceinline__ void token_rows(const AppendRopeArgs &a, int i, int tid, bool early, RopeTab *s_tab) {
     constexpr int kBatch = 2;
     const int j = tid & 7, slot = tid >> 3;
     const bool has_new = kKv && i < a.kv.total_new, has_q = i < a.total_q;
@@ -221,11 +227,11 @@ __device__ __forceinline__ void token_rows(const AppendRopeArgs &a, int i, int t
             }
         }
     };
-    load(0);
     uint32_t err = 0;
     Place p{0, -1, 0, false};
-    if (has_new) p = place_of(a.kv, i, err);
-    if (tid < 2 * kPairs) {
+    auto prepare = [&]() {
+        if (has_new) p = place_of(a.kv, i, err);
+        if (tid >= 2 * kPairs) return;
         const int pair = tid & (kPairs - 1);
         const bool is_q = tid >= kPairs;
         if (pair < (r.rotary_dim >> 1) && (is_q ? has_q : has_new)) {
@@ -235,10 +241,13 @@ __device__ __forceinline__ void token_rows(const AppendRopeArgs &a, int i, int t
             else if (a.pos_new) pos = __ldg(a.pos_new + (size_t)axis * a.kv.total_new + i);
             put_cs(s_tab[is_q], pair, rope_cs(pos, turns_q64(__ldg(r.inv_freq + pair)), r.scale));
         }
-    }
+    };
+    if (early) prepare();
+    pdl_wait();
+    load(0);
+    if (!early) prepare();
     if (err) set_err(a.kv.dev_err, err);
     __syncthreads();
-    pdl_wait();
     for (int base = 0; base < rows; base += kBatch * kSlots) {
         if (base) load(base);
 #pragma unroll
@@ -268,8 +277,8 @@ __device__ __forceinline__ void token_rows(const AppendRopeArgs &a, int i, int t
         }
     }
     if (has_new && a.kv.kc_new && p.page >= 0 && p.ends_block && tid < kIdxDim / 16)
-        reinterpret_cast<uint4 *>(a.kv.kc_pool)[(size_t)p.page * (kIdxDim / 16) + tid] =
-            __ldg(reinterpret_cast<const uint4 *>(a.kv.kc_new) + (size_t)i * (kIdxDim / 16) + tid);
+        reinterpret_cast<int4 *>(a.kv.kc_pool)[(size_t)p.page * (kIdxDim / 16) + tid] =
+            ld_ordered(reinterpret_cast<const int4 *>(a.kv.kc_new) + (size_t)i * (kIdxDim / 16) + tid);
 }
 
 // ------------------------------------------------------------------ E4M3 cache
@@ -368,7 +377,7 @@ __device__ __forceinline__ Item find_item(const AppendRopeArgs &a, int item) {
 // One item by the CTA.  A pass takes as many heads as fit 64 rows -- one head of
 // a full tile, all heads of a decode token -- and holds their values in
 // registers between the maximum and the stores, so the new rows are read once.
-__device__ __forceinline__ void tile_rows(const AppendRopeArgs &a, int item, RopeTab *s_tab) {
+__device__ __forceinline__ void tile_rows(const AppendRopeArgs &a, int item, bool early, RopeTab *s_tab) {
     __shared__ int s_pos[kMaxAxes][kBlockSize];
     __shared__ uint32_t s_amax[kPassRows];
     __shared__ float s_old[kPassRows], s_new[kPassRows];
@@ -406,9 +415,9 @@ __device__ __forceinline__ void tile_rows(const AppendRopeArgs &a, int item, Rop
             raw1 = reinterpret_cast<const uint4 *>(mine + hb * kHeadDim)[c1];
         }
     };
-    fetch(it.h_begin, per_pass);   // on their way while the tables form
     uint32_t err = 0;
-    if (rotated) {
+    auto tables = [&]() {
+        if (!rotated) return;
         for (int e = tid; e < r.num_axes * cnt; e += kTileThreads) {
             const int axis = e / cnt, tok = e - axis * cnt;
             s_pos[axis][tok] = a.pos_new ? __ldg(a.pos_new + (size_t)axis * kv.total_new + it.i0 + tok)
@@ -422,9 +431,12 @@ __device__ __forceinline__ void tile_rows(const AppendRopeArgs &a, int item, Rop
             for (int tok = tid / kPairs; tok < cnt; tok += kTileThreads / kPairs)
                 put_cs(s_tab[tok], pair, rope_cs(s_pos[axis][tok], f, r.scale));
         }
-    }
-    // the scales and codes held from before, and every store, come after the kernels ahead
+    };
+    if (early) tables();
+    // rows, held scales and codes, and every store, come after the kernels ahead
     pdl_wait();
+    fetch(it.h_begin, per_pass);
+    if (!early) tables();   // the rows are on their way
     for (int hb = it.h_begin; hb < it.h_end; hb += per_pass) {
         const int nh = min(per_pass, it.h_end - hb);
         if (tid < nh) {
@@ -482,7 +494,7 @@ __device__ __forceinline__ void tile_rows(const AppendRopeArgs &a, int item, Rop
                 if (s_old[h] == s_new[h]) continue;
                 const float ratio = s_old[h] / s_new[h];
                 uint4 *w = reinterpret_cast<uint4 *>(pool + ((size_t)tok * H + hb + h) * kHeadDim) + j;
-                uint4 c = *w;   // a plain load stays behind the wait
+                uint4 c = *w;
                 c.x = rescale_e4m3x4(c.x, ratio);
                 c.y = rescale_e4m3x4(c.y, ratio);
                 c.z = rescale_e4m3x4(c.z, ratio);
@@ -496,19 +508,21 @@ __device__ __forceinline__ void tile_rows(const AppendRopeArgs &a, int item, Rop
     const int end = it.t0 + held + cnt;                          // position behind it
     const bool ends_block = end == it.len || (end & ((1 << kv.block_shift) - 1)) == 0;
     if (!it.is_v && it.h_begin == 0 && kv.kc_new && ends_block && tid < kIdxDim / 16)
-        reinterpret_cast<uint4 *>(kv.kc_pool)[(size_t)it.page * (kIdxDim / 16) + tid] =
-            __ldg(reinterpret_cast<const uint4 *>(kv.kc_new) + (size_t)(it.i0 + cnt - 1) * (kIdxDim / 16) + tid);
+        reinterpret_cast<int4 *>(kv.kc_pool)[(size_t)it.page * (kIdxDim / 16) + tid] =
+            ld_ordered(reinterpret_cast<const int4 *>(kv.kc_new) + (size_t)(it.i0 + cnt - 1) * (kIdxDim / 16) + tid);
 }
 
 }  // namespace
 
-__global__ void __launch_bounds__(kThreads, 5) kv_append_rope_kernel(AppendRopeArgs a) {
+// kEarly: the whole grid is its first wave
+template <bool kEarly>
+__global__ void __launch_bounds__(kThreads, kRopeCtas) kv_append_rope_kernel(AppendRopeArgs a) {
     __shared__ RopeTab s_tab[2];
     pdl_trigger();
-    token_rows<true>(a, blockIdx.x, threadIdx.x, s_tab);
+    token_rows<true>(a, blockIdx.x, threadIdx.x, kEarly, s_tab);
 }
 
-__global__ void __launch_bounds__(kTileThreads, 2) kv_append_fp8_kernel(AppendRopeArgs a) {
+__global__ void __launch_bounds__(kTileThreads, kTileCtas) kv_append_fp8_kernel(AppendRopeArgs a) {
     __shared__ RopeTab s_tab[kBlockSize];
     pdl_trigger();
     // append and query CTAs in turn as long as there are both: the former wait on
@@ -516,11 +530,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) kv_append_fp8_kernel(AppendRo
     const int b = blockIdx.x, both = min(a.tile_ctas, (int)gridDim.x - a.tile_ctas);
     const bool appends = b < 2 * both ? !(b & 1) : a.tile_ctas > both;
     const int i = b < 2 * both ? b >> 1 : b - both;
+    const bool early = b < kSms * kTileCtas;
     if (appends) {
-        tile_rows(a, i, s_tab);
+        tile_rows(a, i, early, s_tab);
     } else {   // a query per half of the CTA
         const int half = threadIdx.x / kThreads;
-        token_rows<false>(a, 2 * i + half, threadIdx.x % kThreads, s_tab + 2 * half);
+        token_rows<false>(a, 2 * i + half, threadIdx.x % kThreads, early, s_tab + 2 * half);
     }
     // also where a CTA had nothing to do: whatever waits for this kernel waits
     // for the kernels ahead of it too
@@ -530,7 +545,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) kv_append_fp8_kernel(AppendRo
 cudaError_t launch_kv_append_rope(const AppendRopeArgs &a, cudaStream_t stream) {
     const int ctas = a.kv.total_new > a.total_q ? a.kv.total_new : a.total_q;
     if (ctas == 0) return cudaSuccess;
-    return launch_pdl(kv_append_rope_kernel, dim3(ctas), dim3(kThreads), 0, stream, a);
+    return launch_pdl(ctas <= kSms * kRopeCtas ? kv_append_rope_kernel<true> : kv_append_rope_kernel<false>, dim3(ctas),
+                      dim3(kThreads), 0, stream, a);
 }
 
 cudaError_t launch_kv_append_fp8(const AppendRopeArgs &a, cudaStream_t stream) {

@@ -35,16 +35,18 @@
  *    query heads per KV head 1..16; indexer heads 1..16.  Anything else is
  *    DSA_ERR_UNSUPPORTED.
  *  - Consecutive calls on one stream overlap: each kernel lets the next one
- *    start early (programmatic dependent launch) and waits for its
- *    predecessor before it reads anything a library call writes (the pools,
- *    scores, selections).  Before that wait a kernel may already read the
- *    batch description and its own inputs (block_table, seq_lens, cu_q, q_pos,
- *    k_per_seq, q_idx, w, q, and an append's new rows, positions and rotation):
- *    these must not be outputs of the library call issued just before it on
- *    the same stream.  (One exception: the attention calls read their q after
- *    the wait, so q may come from a dsa_kv_append_rope or dsa_kv_append_fp8
- *    just before.)  Work from other kernels is
- *    waited for in full, as usual.
+ *    start early (programmatic dependent launch) and waits for everything
+ *    ahead of it before it reads what a library call writes (the pools,
+ *    scores, selections), the q of an attention call, or the rows of an append
+ *    (k, v, q and coarse keys).  These may come from any work before the call.
+ *    Before that wait a kernel may already read the batch's description and its
+ *    other inputs: block_table, seq_lens, cu_q, cu_new, q_pos, k_per_seq, q_idx,
+ *    w, and an append's positions and rotation.  Those have to be finished when
+ *    the kernel may start.  They are behind copies and kernels that do not let
+ *    their successors start early.  They are not when they are outputs of a
+ *    library call that only other library calls separate from this one, or of
+ *    any kernel that issues griddepcontrol.launch_dependents itself: put a copy
+ *    or an ordinary kernel between.
  *  - Calls on different streams may run at the same time (independent
  *    batches in flight, one stream each) as long as no call writes what
  *    another reads or writes: each needs its own outputs and workspaces.  The

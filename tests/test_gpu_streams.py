@@ -97,3 +97,64 @@ def test_single_calls_on_a_side_stream(cuda_device):
         for x, y in zip(got, want):
             assert torch.equal(x, y), i
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_append_reads_rows_that_the_kernel_ahead_writes(fp8, cuda_device):
+    """The appended rows and queries are the output of a long kernel just before that lets its
+    successors start early (an attention call), directly and with a short library call between."""
+    T = 600
+    b = Batch((900, 900), (300, 300), 8, 64, seed=102)
+    _, src = b.cache8()
+    sel, cnt = (t.cuda() for t in selection(b, 12))
+    _, cache = b.cache8() if fp8 else b.cache16()
+    _, _, rope = rotary()
+    small = Batch((70,), (1,), 1, 1, seed=103)
+    _, other = small.cache16()
+    # attention output [T][64][128]: heads 0..47 serve as queries, 48..55 as K, 56..63 as V
+    out, lse = torch.empty((T, 64, 128), dtype=torch.bfloat16, device="cuda"), torch.empty((T, 64), device="cuda")
+    q, k, v = out.split([48, 8, 8], dim=1)
+    q_out = torch.empty((T, 48, 128), dtype=torch.bfloat16, device="cuda")
+    state = [cache.k_pool, cache.v_pool] + ([cache.k_scale, cache.v_scale] if fp8 else [])
+    start = [t.clone() for t in state]
+
+    def attention():
+        dsa.sparse_attn_prefill_fp8(src, b.seqs, b.queries, b.dq, sel, cnt, out=out, lse=lse, dev_err=b.err)
+
+    def between():
+        dsa.kv_append_rope(other, small.seqs, small.queries.cu_q, small.dk, small.dv, None, rope, dev_err=b.err)
+
+    def append():
+        (dsa.kv_append_fp8 if fp8 else dsa.kv_append_rope)(
+            cache, b.seqs, b.queries.cu_q, k, v, None, rope, queries=b.queries, q=q, q_out=q_out, dev_err=b.err)
+
+    def restore():
+        out.zero_()
+        q_out.zero_()
+        for t, old in zip(state, start):
+            t.copy_(old)
+        torch.cuda.synchronize()
+
+    restore()
+    attention()
+    torch.cuda.synchronize()
+    append()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in [q_out] + state]
+    assert bool(want[0].any()) and int(b.err) == 0
+    for chain in ((attention, append), (attention, between, append)):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for call in chain:
+                call()
+        for i in range(10):
+            restore()
+            if i % 2:
+                graph.replay()
+            else:
+                for call in chain:
+                    call()
+            torch.cuda.synchronize()
+            for got, w in zip([q_out] + state, want):
+                assert torch.equal(got.view(torch.uint8), w.view(torch.uint8)), i
+    assert int(b.err) == 0
