@@ -304,7 +304,7 @@ def _append_rope(fn: str, cache, seqs: SeqBatch, cu_new, k_new, v_new, kc_new, r
         f8 = isinstance(cache, PagedKVCacheFP8)
         r, qs = rope or _NO_ROPE, queries or _NO_QUERIES
         rc = _native.append(
-            _lib.ADDRESS[fn], dev, _raw_stream(stream, dev), cache.k_pool, cache.v_pool, cache.kc_pool,
+            _lib.ADDRESS[fn], dev, _raw_stream(stream, dev), f8, cache.k_pool, cache.v_pool, cache.kc_pool,
             cache.k_scale if f8 else None, cache.v_scale if f8 else None, seqs.block_table, seqs.seq_lens, cu_new, k_new,
             v_new, kc_new, pos_new, r.inv_freq, r.pair_axis, r.interleaved, r.num_axes, r.scale, qs.cu_q, qs.q_pos, q,
             pos_q, q_out, dev_err)

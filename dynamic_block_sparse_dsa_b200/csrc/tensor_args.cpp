@@ -71,9 +71,9 @@ struct Reader {
     }
 };
 
-// k_pool, v_pool, kc_pool, k_scale, v_scale (None, None: the bf16 cache)
-bool read_cache(Reader &r, PyObject *const *o, dsa_kv_cache &c, dsa_kv_cache_fp8 &c8, bool &fp8) {
-    fp8 = o[3] != Py_None;
+// k_pool, v_pool, kc_pool and, with fp8, k_scale, v_scale.  The caller names the
+// form, the one that its entry point takes: it does not follow from the tensors.
+bool read_cache(Reader &r, bool fp8, PyObject *const *o, dsa_kv_cache &c, dsa_kv_cache_fp8 &c8) {
     const at::ScalarType type = fp8 ? at::kByte : at::kBFloat16;
     const at::ScalarType other = fp8 ? at::kFloat8_e4m3fn : at::ScalarType::Undefined;
     const at::Tensor *k = r.tensor(o[0]), *kc = r.tensor(o[2]);
@@ -113,12 +113,12 @@ bool read_queries(Reader &r, PyObject *cu_q, PyObject *q_pos, dsa_queries &q) {
     return r.good;
 }
 
-// append(call, device, stream, k_pool, v_pool, kc_pool, k_scale, v_scale, block_table, seq_lens, cu_new, k_new,
+// append(call, device, stream, fp8, k_pool, v_pool, kc_pool, k_scale, v_scale, block_table, seq_lens, cu_new, k_new,
 //        v_new, kc_new, pos_new, inv_freq, pair_axis, interleaved, num_axes, scale, cu_q, q_pos, q, pos_q, q_out, dev_err)
-// -> status of dsa_kv_append_rope / dsa_kv_append_fp8 at address `call`, or None
+// -> status of dsa_kv_append_rope (fp8 False) / dsa_kv_append_fp8 (True) at address `call`, or None
 PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     int status = -1;
-    if (n == 26) try {
+    if (n == 27) try {
         Reader r{PyLong_AsLong(a[1])};
         dsa_kv_cache c;
         dsa_kv_cache_fp8 c8;
@@ -127,45 +127,45 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         dsa_rope rope{};
         dsa_queries q{};
         dsa_query_rows w{};
-        bool fp8 = false;
-        if (!read_cache(r, a + 3, c, c8, fp8) || !read_seqs(r, a[8], a[9], s)) Py_RETURN_NONE;
-        const long long axes = PyLong_AsLong(a[18]);
+        const bool fp8 = a[3] == Py_True;
+        if (!read_cache(r, fp8, a + 4, c, c8) || !read_seqs(r, a[9], a[10], s)) Py_RETURN_NONE;
+        const long long axes = PyLong_AsLong(a[19]);
         if (axes < 1 || axes > 4) Py_RETURN_NONE;
-        if (a[11] != Py_None) {
+        if (a[12] != Py_None) {
             long long total, heads, v_total, v_heads;
-            f.k = r.rows(a[11], total, heads, f.k_stride);
-            f.v = r.rows(a[12], v_total, v_heads, f.v_stride);
+            f.k = r.rows(a[12], total, heads, f.k_stride);
+            f.v = r.rows(a[13], v_total, v_heads, f.v_stride);
             if (!r.good || total < 1 || total > INT32_MAX || v_total != total || heads != c.num_kv_heads ||
                 v_heads != heads)
                 Py_RETURN_NONE;
             f.total_new = (int32_t)total;
-            f.cu_new = static_cast<int32_t *>(r.flat(a[10], at::kInt, s.num_seqs + 1ll));
-            f.kc = static_cast<int8_t *>(r.flat_or_null(a[13], at::kChar, total * 64, at::kByte));
-            f.pos = r.positions(a[14], axes, total);
+            f.cu_new = static_cast<int32_t *>(r.flat(a[11], at::kInt, s.num_seqs + 1ll));
+            f.kc = static_cast<int8_t *>(r.flat_or_null(a[14], at::kChar, total * 64, at::kByte));
+            f.pos = r.positions(a[15], axes, total);
         }
-        const bool turns = a[15] != Py_None;
+        const bool turns = a[16] != Py_None;
         if (turns) {
-            rope.inv_freq = static_cast<float *>(r.flat(a[15], at::kFloat));
+            rope.inv_freq = static_cast<float *>(r.flat(a[16], at::kFloat));
             if (!r.good) Py_RETURN_NONE;
-            const long long half = THPVariable_Unpack(a[15]).numel();
-            if (half < 1 || half > 64 || (axes > 1 && a[16] == Py_None)) Py_RETURN_NONE;
-            rope.pair_axis = axes > 1 ? static_cast<int32_t *>(r.flat(a[16], at::kInt, half)) : nullptr;
+            const long long half = THPVariable_Unpack(a[16]).numel();
+            if (half < 1 || half > 64 || (axes > 1 && a[17] == Py_None)) Py_RETURN_NONE;
+            rope.pair_axis = axes > 1 ? static_cast<int32_t *>(r.flat(a[17], at::kInt, half)) : nullptr;
             rope.rotary_dim = (int32_t)(2 * half);
-            rope.layout = PyObject_IsTrue(a[17]) == 1 ? DSA_ROPE_PAIRS : DSA_ROPE_HALVES;
+            rope.layout = PyObject_IsTrue(a[18]) == 1 ? DSA_ROPE_PAIRS : DSA_ROPE_HALVES;
             rope.num_axes = (int32_t)axes;
-            rope.scale = (float)PyFloat_AsDouble(a[19]);
+            rope.scale = (float)PyFloat_AsDouble(a[20]);
         }
-        const bool has_q = a[22] != Py_None;
+        const bool has_q = a[23] != Py_None;
         if (has_q) {
             long long tokens, heads;
-            if (!turns || !read_queries(r, a[20], a[21], q)) Py_RETURN_NONE;
-            w.q = r.rows(a[22], tokens, heads, w.q_stride);
+            if (!turns || !read_queries(r, a[21], a[22], q)) Py_RETURN_NONE;
+            w.q = r.rows(a[23], tokens, heads, w.q_stride);
             if (!r.good || tokens != q.total_q || heads > INT32_MAX) Py_RETURN_NONE;
             w.num_heads = (int32_t)heads;
-            w.pos = r.positions(a[23], axes, tokens);
-            w.out = r.like(a[24], at::kBFloat16, a[22], 3);
+            w.pos = r.positions(a[24], axes, tokens);
+            w.out = r.like(a[25], at::kBFloat16, a[23], 3);
         }
-        int32_t *err = static_cast<int32_t *>(r.flat_or_null(a[25], at::kInt, -1));
+        int32_t *err = static_cast<int32_t *>(r.flat_or_null(a[26], at::kInt, -1));
         if (!r.good || PyErr_Occurred()) {
             PyErr_Clear();
             Py_RETURN_NONE;
@@ -199,8 +199,7 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
         dsa_kv_cache_fp8 c8;
         dsa_seqs s;
         dsa_queries q;
-        bool fp8 = false;
-        if (!read_cache(r, a + 3, c, c8, fp8) || !fp8 || !read_seqs(r, a[8], a[9], s) || !read_queries(r, a[10], a[11], q))
+        if (!read_cache(r, true, a + 3, c, c8) || !read_seqs(r, a[8], a[9], s) || !read_queries(r, a[10], a[11], q))
             Py_RETURN_NONE;
         if (THPVariable_Unpack(a[10]).numel() != s.num_seqs + 1ll) Py_RETURN_NONE;
         long long tokens, heads;

@@ -2,6 +2,7 @@
 import contextlib
 import ctypes
 
+import pytest
 import torch
 
 import dynamic_block_sparse_dsa_b200 as dsa
@@ -87,3 +88,32 @@ def test_allocations_are_made_on_the_calls_stream(monkeypatch):
                                            wl.k_per_seq, 4, wl.q))):
         call(*args, stream=stream)
         check()
+
+
+def test_the_native_reader_takes_the_form_of_the_entry_point(monkeypatch):
+    """A PagedKVCacheFP8 without scales over bf16 pools is refused before any call: the 8-bit entry
+    point would read past the bf16 cache's description."""
+    if dsa._native is None:
+        pytest.skip("the native reader is not built here")
+    calls = []
+    entry = ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_void_p] * 8)(lambda *a: calls.append(a) or 0)
+    at = ctypes.cast(entry, ctypes.c_void_p).value
+    dsa.load()
+    for name in ("dsa_kv_append_rope", "dsa_kv_append_fp8"):
+        monkeypatch.setitem(dsa._lib.ADDRESS, name, at)
+    monkeypatch.setattr(dsa, "_current", lambda t: -1)
+    monkeypatch.setattr(dsa, "_raw_stream", lambda s, dev: 0)
+    pool = torch.zeros(2, 64, 1, 128, dtype=torch.bfloat16)
+    code, kc, scale = torch.zeros(2, 64, 1, 128, dtype=torch.uint8), torch.zeros(2, 64, dtype=torch.int8), torch.ones(2, 1, 1)
+    seqs = dsa.SeqBatch(torch.zeros(1, 2, dtype=torch.int32), torch.ones(1, dtype=torch.int32))
+    cu, row = torch.tensor([0, 1], dtype=torch.int32), torch.zeros(1, 1, 128, dtype=torch.bfloat16)
+    for bad in (dsa.PagedKVCacheFP8(pool, pool, kc, None, None), dsa.PagedKVCacheFP8(pool, pool, kc, scale, scale),
+                dsa.PagedKVCacheFP8(code, code, kc, None, None), dsa.PagedKVCacheFP8(code, code, kc, scale, None)):
+        with pytest.raises((ValueError, AttributeError)):
+            dsa.kv_append_fp8(bad, seqs, cu, row, row)
+    with pytest.raises(ValueError):
+        dsa.kv_append_rope(dsa.PagedKVCache(code, code, kc), seqs, cu, row, row, None, dsa.Rotary(torch.ones(64)))
+    assert not calls
+    dsa.kv_append_fp8(dsa.PagedKVCacheFP8(code, code, kc, scale, scale), seqs, cu, row, row)
+    dsa.kv_append_rope(dsa.PagedKVCache(pool, pool, kc), seqs, cu, row, row, None, dsa.Rotary(torch.ones(64)))
+    assert len(calls) == 2
