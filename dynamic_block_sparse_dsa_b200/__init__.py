@@ -39,7 +39,7 @@ from typing import Optional
 
 import torch
 
-from . import _lib
+from . import _args, _lib
 from ._args import HEAD_DIM, _at, _rows, _wrong_device, native as _native
 from ._lib import DsaError, load
 
@@ -51,6 +51,18 @@ __all__ = [
     "index_score_fp8", "topk_blocks_i64", "PagedKVCacheFP8", "Rotary", "kv_append_rope", "kv_append_fp8",
     "sparse_attn_decode_fp8", "sparse_attn_prefill_fp8",
 ]
+
+
+
+def _connect() -> None:
+    """Build the native reader with the library where it is missing, and use it from then on."""
+    global _native, _at, _rows
+    if _args.native is None:
+        _args.connect(build=True)
+        _native, _at, _rows = _args.native, _args._at, _args._rows
+
+
+_lib.on_load.append(_connect)
 
 BLOCK_SIZE = 64
 IDX_DIM = 64

@@ -1,12 +1,16 @@
 """Reading tensor arguments: address, type, device and layout checks.
 
 The functions here define what a call accepts.  Where the native reader
-(csrc/tensor_args.cpp) is built for this torch, it answers the ordinary case
-and hands everything else to them.
+(csrc/tensor_args.cpp) is built, it answers the ordinary case and hands
+everything else to them.
 """
 from __future__ import annotations
 
+import sys
+
 import torch
+
+from . import build as _build
 
 HEAD_DIM = 128
 
@@ -54,11 +58,24 @@ def _rows(t: torch.Tensor, dev: int, name: str):
 py_at, py_rows = _at, _rows   # what the native reader falls back to
 
 native = None   # the native reader's module
-try:
-    from . import _tensor_args
-    if _tensor_args.torch_version == torch.__version__.split("+")[0]:
-        native = _tensor_args
-        native.use(py_at, py_rows)
-        _at, _rows = native.at, native.rows
-except ImportError:   # not built, or built for another Python or torch
-    pass
+
+
+def connect(build: bool = False) -> None:
+    """Put the native reader into use, if it is built from the sources that are here for this
+    torch and Python; with ``build``, it is built first where it is not."""
+    global native, _at, _rows
+    if native is not None or (_build.args_stale() and not (build and _build.build_tensor_args())):
+        return
+    try:
+        from . import _tensor_args
+    except ImportError as e:
+        sys.stderr.write(f"the native reader of tensor arguments does not load: {e}\n")
+        return
+    if _tensor_args.built_from != _build.args_key():   # one that this process had loaded before it was built anew
+        return
+    native = _tensor_args
+    native.use(py_at, py_rows)
+    _at, _rows = native.at, native.rows
+
+
+connect()

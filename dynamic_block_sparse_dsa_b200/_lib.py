@@ -17,6 +17,7 @@ from . import build as _build
 _lock = threading.Lock()
 _lib = None
 ADDRESS = {}   # entry point -> its address, once the library is loaded
+on_load = []   # called once the library is loaded
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_RANGE, DSA_ERR_WORKSPACE, DSA_ERR_CUDA = range(6)
 DEV_ERR_PAGE, DEV_ERR_POS, DEV_ERR_SEL, DEV_ERR_K, DEV_ERR_WAIT, DEV_ERR_VALUE = 1, 2, 4, 8, 16, 32
@@ -145,7 +146,9 @@ def load():
             f.restype = rest
             ADDRESS[name] = ctypes.cast(f, c_vp).value
         _lib = lib
-        return lib
+    for f in on_load:
+        f()
+    return lib
 
 
 def check(fn: str, status: int) -> None:

@@ -6,17 +6,20 @@ it with ctypes.  Run ``python -m dynamic_block_sparse_dsa_b200.build``.
 from __future__ import annotations
 
 import glob
+import hashlib
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdsa.so")
 ARGS_SRC = os.path.join(CSRC, "tensor_args.cpp")
-ARGS_LIB = os.path.join(PKG, "_tensor_args.so")
+ARGS_LIB = os.path.join(PKG, "_tensor_args" + sysconfig.get_config_var("EXT_SUFFIX"))   # for this Python alone
+HEADER = os.path.join(ROOT, "include", "dsa.h")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -33,7 +36,7 @@ def sources() -> list:
 
 def _inputs() -> list:
     return sources() + sorted(glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))) + \
-        [os.path.join(ROOT, "include", "dsa.h"), os.path.abspath(__file__)]
+        [HEADER, os.path.abspath(__file__)]
 
 
 def is_stale() -> bool:
@@ -43,30 +46,60 @@ def is_stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
-def build_tensor_args(force: bool = False) -> bool:
-    """Compile the binding's native tensor reader beside libdsa.so.  The binding
-    does the same in Python without it, so a failure here is only reported."""
-    if not force and os.path.exists(ARGS_LIB) and os.path.getmtime(ARGS_LIB) >= os.path.getmtime(ARGS_SRC):
-        return True
-    import sysconfig
-
+def _args_command() -> list:
+    """The compiler and its arguments, without the output, for the reader of tensor arguments."""
     import torch
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"]]
-    tmp = ARGS_LIB + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[a for i in inc for a in ("-isystem", i)],
-           "-o", tmp, ARGS_SRC, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[a for i in inc for a in ("-isystem", i)], ARGS_SRC, "-L" + os.path.join(root, "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-lc10"]
+
+
+def args_key() -> str:
+    """Names what the reader is built from: its source, the structs that it fills, the command, torch and Python."""
+    import torch
+    h = hashlib.sha256(repr((_args_command(), torch.__version__, torch.version.git_version, sys.version)).encode())
+    for path in (ARGS_SRC, HEADER):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()[:32]
+
+
+def args_stale() -> bool:
+    """Whether the reader is missing or built from anything else than what is here."""
     try:
-        r = subprocess.run(cmd, capture_output=True, text=True)
+        with open(ARGS_LIB + ".key") as f:
+            return not os.path.exists(ARGS_LIB) or f.read() != args_key()
+    except OSError:
+        return True
+
+
+def build_tensor_args(force: bool = False) -> bool:
+    """Compile the binding's native tensor reader beside libdsa.so.  The binding
+    does the same in Python without it, so a failure here is only reported."""
+    if not force and not args_stale():
+        return True
+    tmp = ARGS_LIB + f".tmp{os.getpid()}"
+    try:
+        key = args_key()
+        r = subprocess.run([*_args_command(), f'-DDSA_ARGS_KEY="{key}"', "-o", tmp], capture_output=True, text=True)
     except OSError as e:
         sys.stderr.write(f"tensor_args.cpp not built: {e}\n")
         return False
     if r.returncode != 0:
         sys.stderr.write(f"tensor_args.cpp not built ({r.returncode}):\n{r.stderr[-2000:]}\n")
         return False
+    try:   # no key stands beside a reader that it does not belong to
+        os.remove(ARGS_LIB + ".key")
+    except OSError:
+        pass
     os.replace(tmp, ARGS_LIB)
+    with open(tmp, "w") as f:
+        f.write(key)
+    os.replace(tmp, ARGS_LIB + ".key")
     return True
 
 

@@ -9,7 +9,6 @@
 
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
-#include <torch/version.h>
 
 #include "../../include/dsa.h"
 
@@ -303,7 +302,7 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_tensor_args", nullptr, -1, g_me
 
 PyMODINIT_FUNC PyInit__tensor_args(void) {
     PyObject *m = PyModule_Create(&g_module);
-    // the binding loads it only beside the torch it was built with
-    if (m) PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION);
+    // what it was built from (build.py): the binding uses it only beside that
+    if (m) PyModule_AddStringConstant(m, "built_from", DSA_ARGS_KEY);
     return m;
 }

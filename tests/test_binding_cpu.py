@@ -1,11 +1,14 @@
-"""The binding without a device: where a call's allocations are made."""
+"""The binding without a device: where a call's allocations are made, what the
+native reader takes, when it is built."""
 import contextlib
 import ctypes
+import sysconfig
 
 import pytest
 import torch
 
 import dynamic_block_sparse_dsa_b200 as dsa
+from dynamic_block_sparse_dsa_b200 import build
 from dynamic_block_sparse_dsa_b200 import workloads as wk
 
 
@@ -117,3 +120,47 @@ def test_the_native_reader_takes_the_form_of_the_entry_point(monkeypatch):
     dsa.kv_append_fp8(dsa.PagedKVCacheFP8(code, code, kc, scale, scale), seqs, cu, row, row)
     dsa.kv_append_rope(dsa.PagedKVCache(pool, pool, kc), seqs, cu, row, row, None, dsa.Rotary(torch.ones(64)))
     assert len(calls) == 2
+
+
+# ----------------------------------------------------------------------------- the native reader's build
+
+def test_the_reader_is_stale_when_anything_it_is_built_from_changes(monkeypatch, tmp_path):
+    """Its source, the header whose structs it fills, torch: each makes a built reader stale; and its
+    file is named for this Python."""
+    if not build.build_tensor_args():
+        pytest.skip("no C++ compiler here")
+    assert not build.args_stale()
+    assert build.ARGS_LIB.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    for name in ("HEADER", "ARGS_SRC"):
+        with monkeypatch.context() as m:
+            other = tmp_path / name
+            other.write_text(open(getattr(build, name)).read() + "\n/* another field */\n")
+            m.setattr(build, name, str(other))
+            assert build.args_stale()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.1")
+        assert build.args_stale()
+    assert not build.args_stale()
+
+
+def test_a_stale_reader_is_not_used_and_one_built_here_is(monkeypatch):
+    from dynamic_block_sparse_dsa_b200 import _args
+    if _args.native is None and not build.build_tensor_args():
+        pytest.skip("no C++ compiler here")
+    for m, names in ((_args, ("native", "_at", "_rows")), (dsa, ("_native", "_at", "_rows"))):
+        for n in names:
+            monkeypatch.setattr(m, n, None)
+    monkeypatch.setattr(build, "args_stale", lambda: True)
+    monkeypatch.setattr(build, "build_tensor_args", lambda: False)
+    _args.connect()
+    dsa._connect()
+    assert _args.native is None and dsa._native is None      # stale, and not to be built
+    monkeypatch.setattr(build, "build_tensor_args", lambda: True)
+    _args.connect()
+    assert _args.native is None                              # an import builds nothing
+    dsa._connect()                                           # as load() does
+    assert _args.native is not None and dsa._native is _args.native and dsa._at is _args.native.at
+    monkeypatch.setattr(_args, "native", None)
+    monkeypatch.setattr(build, "args_key", lambda: "another")
+    _args.connect(build=True)
+    assert _args.native is None                              # the module in this process is not the one just built
