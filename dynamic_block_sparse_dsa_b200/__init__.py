@@ -207,6 +207,8 @@ class PagedKVCacheFP8:
     def index_ctype(self) -> _lib.KvCacheC:
         """What the indexer and selection calls read: the coarse keys and the sizes."""
         n, bs, hkv, d = self.k_pool.shape
+        if self.kc_pool.element_size() != 1 or self.kc_pool.shape[0] != n:
+            raise ValueError("kc_pool must hold one byte per element and one row per page")
         return _lib.KvCacheC(_addr(self.k_pool), _addr(self.v_pool), _addr(self.kc_pool), n, bs, hkv, d,
                              self.kc_pool.shape[1])
 

@@ -164,3 +164,19 @@ def test_a_stale_reader_is_not_used_and_one_built_here_is(monkeypatch):
     monkeypatch.setattr(build, "args_key", lambda: "another")
     _args.connect(build=True)
     assert _args.native is None                              # the module in this process is not the one just built
+
+
+def test_selection_over_the_8bit_cache_checks_the_coarse_keys():
+    """The indexer and selection calls read one 64-byte row per page: a kc_pool of wider elements or
+    of fewer rows would be read as something else, or past its end."""
+    code, scale = torch.zeros(2, 64, 1, 128, dtype=torch.uint8), torch.ones(2, 1, 1)
+    seqs = dsa.SeqBatch(torch.zeros(1, 2, dtype=torch.int32), torch.ones(1, dtype=torch.int32))
+    queries = dsa.QueryBatch(torch.tensor([0, 1], dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+    q_idx, w = torch.zeros(1, 4, 64, dtype=torch.int8), torch.zeros(1, 4, dtype=torch.int32)
+    kps = torch.ones(1, dtype=torch.int32)
+    for kc in (torch.zeros(1, 64, dtype=torch.int8), torch.zeros(2, 64, dtype=torch.int32)):
+        cache = dsa.PagedKVCacheFP8(code, code, kc, scale, scale)
+        for call in (lambda: dsa.index_score(cache, seqs, queries, q_idx, w),
+                     lambda: dsa.select_blocks(cache, seqs, queries, q_idx, w, kps, 1, workspace=torch.zeros(1))):
+            with pytest.raises(ValueError, match="one row per page"):
+                call()
