@@ -150,15 +150,17 @@ void attn_schedule(AttnArgs &a, bool allow_split, bool allow_cluster = false) {
 // rounds of one pair per warp while there are pairs for every warp, then teams
 // for the pairs left over.  (An even split of the tiles over all CTAs, with a
 // merge of eight warps for every pair a CTA touches, took 33.9 us for 64 short
-// contexts and 15.3 us for 8 long ones; the teams take 26.2 and 11.5 us.)
+// contexts and 15.3 us for 8 long ones; the teams take 26.6 and 11.7 us.)
 void attn_schedule_fp8(AttnArgs &a, bool allow_split) {
     long long C = sm_count();
     if (C > kAttnMaxCtas) C = kAttnMaxCtas;
     const long long pairs = (long long)a.total_q * a.num_kv_heads;
     // 12 warps hide more latency where every warp has a pair of its own (4096-query
-    // chunk 2.63 ms, 333 queries 113 us; with 8 warps 3.00 ms, 125 us); 8 divide a
-    // decode batch better (8 long contexts 11.6 us, 64 short ones 26.5 us; with 12
-    // warps 12.7 us, 29.5 us)
+    // chunk of 8 KV heads 2.40 ms, 1000 queries 179 us, 333 queries 105 us, 222
+    // queries, the least here, 41 us; with 8 warps 2.85 ms, 192, 117 and 47 us); 8
+    // divide smaller batches better as a rule (8 long contexts 11.7 us, 64 short
+    // ones 26.6 us, 148 queries 31 us; with 12 warps 13.5, 30.6 and 41 us; but 100
+    // queries take 31 us with 8 and 27 us with 12)
     const int warps = pairs < C * kFp8ManyWarps || a.group > 8 ? kFp8Warps : kFp8ManyWarps;
     const long long W = C * warps;
     a.warps = warps;
@@ -741,9 +743,12 @@ int dsa_kv_append_fp8(const dsa_kv_cache_fp8 *cache, const dsa_seqs *seqs, const
     if (rc) return rc;
     a.k_scale = cache->k_scale;
     a.v_scale = cache->v_scale;
-    // heads that share a tile's rotation tables, one after the other: with 4 (2)
-    // instead of 8, 64 decode tokens and two 2048-token chunks of 8 heads took 32.4
-    // (37.4) us instead of 30.4
+    // heads that share a tile's rotation tables, one after the other.  Fewer make
+    // more items, each with tables of its own: with 4 (2) instead of 8, of 8 heads,
+    // 64 decode tokens and two 2048-token chunks take 33.0 (36.6) us instead of 31.0,
+    // 4096 tokens 22.1 (24.4) instead of 21.2, 32 decode tokens 2.9 (4.5) instead of
+    // 2.3.  A single short chunk has fewer items than the GPU has room for and loses:
+    // 512 tokens 15.0 us, with 4 (2) 8.2 (4.9); 128 tokens 10.8, 6.2 (3.8).
     a.heads_per_item = 8;
     const long long units = a.kv.total_new > 0 ? a.kv.total_new / kBlockSize + 2ll * a.kv.num_seqs : 0;
     const long long groups = (a.kv.num_kv_heads + a.heads_per_item - 1) / a.heads_per_item;

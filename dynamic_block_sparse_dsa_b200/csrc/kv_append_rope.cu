@@ -29,11 +29,13 @@
 // Work and bounds (one B200).  The bf16 kernel runs a CTA of 256 threads per
 // token: its K, V and query rows, 32 bytes a thread and row, with the rows'
 // loads issued before the (cos, sin) table is ready.  4096 tokens of 64 query
-// and 8 KV heads take 28.5 us, 5.9 TB/s of rows read and written (0.90 of the
-// copy bandwidth): memory-bound.  The E4M3 kernel runs a CTA of 512 threads per
+// and 8 KV heads take 31.3 us in calls back to back, 5.4 TB/s of rows read and
+// written (0.82 of the copy bandwidth): memory-bound, with a gap between the
+// calls (28.6 us when the next call's loads filled it, before its wait).  The
+// E4M3 kernel runs a CTA of 512 threads per
 // (tile, K or V, up to eight heads) and per two queries: the first wait on
 // tables, maxima and barriers, the second on memory, and they share the SMs.
-// 4160 tokens (64 of them decode tokens) take 30.3 us, 5.3 TB/s (0.82); 32 decode
+// 4160 tokens (64 of them decode tokens) take 30.9 us, 5.2 TB/s (0.80); 32 decode
 // tokens take 2.3 us back to back.
 #include "dsa_kernels.h"
 

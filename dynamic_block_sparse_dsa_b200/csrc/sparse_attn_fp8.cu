@@ -55,7 +55,7 @@
 // takes 2.40 ms: 680 instructions a tile, of them 256 conversions at two cycles
 // each, keep the ALU pipe 55 % and the tensor pipe 41 % busy; the gather alone
 // takes 1.67 ms (20 TB/s).  Decode reads its tiles once: 64 contexts of 8K, 135
-// MB, take 26.7 us (5.1 TB/s, 0.77 of the copy bandwidth) and 25.1 us without the
+// MB, take 26.6 us (5.1 TB/s, 0.78 of the copy bandwidth) and 25.1 us without the
 // arithmetic.
 #include "dsa_kernels.h"
 #include "dsa_tma.cuh"
