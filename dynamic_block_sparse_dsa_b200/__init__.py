@@ -110,7 +110,12 @@ def _raw_stream(stream, dev: int) -> int:
 
 def _on(stream):
     """Allocations of a call on ``stream`` belong to that stream."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream))
+
+
+def _torch_stream(stream):
+    """A call's ``stream`` may be anything with the handle in ``cuda_stream``."""
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream)
 
 
 def _workspace(size: int, dev, stream) -> torch.Tensor:
@@ -833,7 +838,7 @@ class PreparedStep:
         self.calls = rec.calls
         if any(t.is_cuda for n, t in self.bufs.items() if n not in had) and not torch.cuda.is_current_stream_capturing():
             # new workspaces are zero before a call on any stream
-            (torch.cuda.current_stream() if stream is None else stream).synchronize()
+            (torch.cuda.current_stream() if stream is None else _torch_stream(stream)).synchronize()
         if stager is not None:
             lib = _lib.load()
             self._stager = stager

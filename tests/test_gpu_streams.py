@@ -158,3 +158,20 @@ def test_append_reads_rows_that_the_kernel_ahead_writes(fp8, cuda_device):
             for got, w in zip([q_out] + state, want):
                 assert torch.equal(got.view(torch.uint8), w.view(torch.uint8)), i
     assert int(b.err) == 0
+
+
+def test_a_stream_is_whatever_holds_its_handle(cuda_device):
+    """A call's stream may be any object with the handle in cuda_stream, also where the call allocates."""
+    class Handle:
+        def __init__(self, s):
+            self.cuda_stream = s.cuda_stream
+
+    b, cache, args = _step_case(True, seed=104)
+    want = {k: v.clone() for k, v in dsa.step(cache, b.seqs, b.queries, **args).items()}
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for got in (dsa.step(cache, b.seqs, b.queries, stream=Handle(side), **args),
+                dsa.PreparedStep(cache, b.seqs, b.queries, stream=Handle(side), **args)()):
+        side.synchronize()
+        for n in ("sel", "cnt", "out", "lse", "q_rot"):
+            assert torch.equal(got[n].view(torch.uint8), want[n].view(torch.uint8)), n

@@ -132,3 +132,38 @@ def test_fused_decode_workspace_serves_batches_of_any_size(cuda_device):
         call, want = calls[key]
         for got, w in zip(call(ws), want):
             assert torch.equal(got, w), (n, key)
+
+
+def test_captured_calls_of_several_batches_share_a_workspace(cuda_device):
+    """Graphs of differently sized batches over both caches, captured on one workspace and replayed
+    in turn with an eager call among them."""
+    keys = [(8, 8, 8, True), (9, 8, 8, True), (40, 8, 8, False), (3, 1, 16, True)]
+    cases, need = [], 0
+    for i, (T, hkv, group, fp8) in enumerate(keys):
+        b = Batch(tuple(1500 + 61 * j for j in range(T)), (1,) * T, hkv, hkv * group, seed=110 + i)
+        cache = (b.cache8() if fp8 else b.cache16())[1]
+        q = torch.randn(T, hkv * group, 128, generator=b.gen).bfloat16().cuda()
+        sel, cnt = (t.cuda() for t in selection(b, 16))
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        fn = dsa.sparse_attn_decode_fp8 if fp8 else dsa.sparse_attn_decode
+        size = dsa.decode_workspace_size(T, hkv * group, hkv, 16)
+
+        def call(ws, fn=fn, b=b, cache=cache, q=q, sel=sel, cnt=cnt, out=out, lse=lse):
+            fn(cache, b.seqs, b.queries, q, sel, cnt, out=out, lse=lse, workspace=ws, dev_err=b.err)
+
+        call(torch.zeros(size, dtype=torch.uint8, device="cuda"))
+        cases.append((call, out, lse, out.clone(), lse.clone(), b.err))
+        need = max(need, size)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graphs = []
+    for call, *_ in cases:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(ws)
+    for n, i in enumerate((0, 1, 2, 0, 3, 1, 2, 3, 1, 0, 2)):
+        call, out, lse, want, want_lse, err = cases[i]
+        out.fill_(7)
+        lse.fill_(7)
+        call(ws) if n % 4 == 3 else graphs[i].replay()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse) and int(err) == 0, (n, i)
